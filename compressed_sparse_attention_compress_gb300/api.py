@@ -64,6 +64,9 @@ def _load():
         "csa_quantize_fp8": [P, P, ctypes.c_int64, I, I, P, P, P],
         "csa_indexer_topk_fp8": [P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, P, P],
         "csa_indexer_kl": [P, P, P, P, P, P, P, I, P, P, P, I, I, I, I, I, I, I, I, F, I, P, P, P, P, Z, P],
+        "csa_cache_write": [P, P, P, P, P, P, I, I, I, P],
+        "csa_cache_read": [P, P, P, P, I, I, I, P, P, P],
+        "csa_cache_attn_fwd": [P, P, P, P, P, I, P, P, P, P, I, I, I, I, I, I, F, I, P, P, P, Z, P],
         "csa_indexer_kl_static_scratch": [P, P, P, P, P, P, P, I, P, P, P, I, I, I, I, I, I, I, I, F, I, P, P, P, P],
     }
     for name, args in sig.items():
@@ -74,6 +77,8 @@ def _load():
     lib.csa_status_string.restype = ctypes.c_char_p
     lib.csa_indexer_kl_workspace.argtypes = [I]
     lib.csa_indexer_kl_workspace.restype = Z
+    lib.csa_cache_attn_workspace.argtypes = [P, I, I, I, I]
+    lib.csa_cache_attn_workspace.restype = Z
     return lib
 
 
@@ -315,3 +320,115 @@ def csa_indexer_topk_fp8(h: Handle, qI, qI_scale, w, kI, kI_scale, cu_seqlens, c
         h.ptr, _p(qI), _p(qI_scale), _p(w), _p(kI), _p(kI_scale), _p(cu_seqlens), _p(cu_cmp),
         cu_seqlens.numel() - 1, T_cap, int(max_seqlen), H_I, d_I, int(ratio), int(topk), idx.shape[1],
         _dtype(w), _p(idx), _stream(stream)))
+
+
+# ---- serving: the paged 8-bit cache ----------------------------------------
+class _CacheStruct(ctypes.Structure):
+    """csa_cache_t."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("table", ctypes.c_void_p), ("n_blocks", ctypes.c_int),
+                ("max_blocks", ctypes.c_int), ("block", ctypes.c_int), ("H_kv", ctypes.c_int), ("d", ctypes.c_int)]
+
+
+def _want(what, t, dtype, shape, device=None):
+    """t is a contiguous tensor of this type and shape (None: any extent) on this device."""
+    if t.dtype != dtype:
+        raise TypeError(f"{what}: {t.dtype}, expected {dtype}")
+    if len(t.shape) != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape)):
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)} (None: any)")
+    if not t.is_contiguous():
+        raise ValueError(f"{what}: tensors passed to libcsa must be contiguous")
+    if device is not None and t.get_device() != device:
+        raise ValueError(f"{what}: on {t.device}, expected cuda:{device}")
+    return t.data_ptr()
+
+
+class Cache:
+    """A paged E4M3 cache over the caller's tensors (held, not copied).
+
+    k (and v, unless V = K): uint8 [n_blocks, H_kv, block, d]; k_scale, v_scale:
+    float32 [n_blocks, H_kv]; table: int32 [B, max_blocks], the blocks of each
+    sequence in order.  Rows of ``table`` may be rewritten in place between calls.
+    """
+
+    def __init__(self, k, k_scale, table, v=None, v_scale=None):
+        if not k.is_cuda:
+            raise ValueError("k: the cache lives on a CUDA device")
+        if (v is None) != (v_scale is None):
+            raise ValueError("v and v_scale come together")
+        n, H_kv, block, d = k.shape
+        dev = k.get_device()
+        s = _CacheStruct()
+        s.k = _want("k", k, torch.uint8, (n, H_kv, block, d), dev)
+        s.k_scale = _want("k_scale", k_scale, torch.float32, (n, H_kv), dev)
+        s.table = _want("table", table, torch.int32, (None, None), dev)
+        if v is not None:
+            s.v = _want("v", v, torch.uint8, (n, H_kv, block, d), dev)
+            s.v_scale = _want("v_scale", v_scale, torch.float32, (n, H_kv), dev)
+        s.n_blocks, s.max_blocks, s.block, s.H_kv, s.d = n, table.shape[1], block, H_kv, d
+        self.k, self.k_scale, self.table, self.v, self.v_scale = k, k_scale, table, v, v_scale
+        self.device, self.B, self.H_kv, self.d = dev, table.shape[0], H_kv, d
+        self._struct = s
+        self._ref = ctypes.addressof(s)
+
+
+def _stream_of(h, stream):
+    return (stream if stream is not None else torch.cuda.current_stream(h.device)).cuda_stream
+
+
+def _packing(h, cache, cu_seqlens, pos0):
+    """Checked sequences of a cache call: (B, cu pointer, pos0 pointer)."""
+    B = cu_seqlens.numel() - 1
+    if cache.device != h.device:
+        raise ValueError(f"cache on cuda:{cache.device}, handle on cuda:{h.device}")
+    if B < 0 or cache.B < B:
+        raise ValueError(f"table has {cache.B} rows for {B} sequences")
+    return (B, _want("cu_seqlens", cu_seqlens, torch.int32, (B + 1,), h.device),
+            _want("pos0", pos0, torch.int32, (B,), h.device))
+
+
+def csa_cache_write(h: Handle, cache: Cache, x_k, cu_seqlens, pos0, x_v=None, stream=None):
+    """Quantise rows [T_cap, H_kv, d] into the cache at positions pos0[b] + i."""
+    B, cu, p0 = _packing(h, cache, cu_seqlens, pos0)
+    shape = (x_k.shape[0], cache.H_kv, cache.d)
+    k = _want("x_k", x_k, x_k.dtype, shape, h.device)
+    v = _want("x_v", x_v, x_k.dtype, shape, h.device) if x_v is not None else None
+    return _check("csa_cache_write", LIB.csa_cache_write(
+        h.ptr, cache._ref, k, v, cu, p0, B, shape[0], _dtype(x_k), _stream_of(h, stream)))
+
+
+def csa_cache_read(h: Handle, cache: Cache, cu_seqlens, pos0, k_out, v_out=None, stream=None):
+    """Rows at positions pos0[b] + i of the cache, dequantised into [T_cap, H_kv, d]."""
+    B, cu, p0 = _packing(h, cache, cu_seqlens, pos0)
+    shape = (k_out.shape[0], cache.H_kv, cache.d)
+    k = _want("k_out", k_out, k_out.dtype, shape, h.device)
+    v = _want("v_out", v_out, k_out.dtype, shape, h.device) if v_out is not None else None
+    return _check("csa_cache_read", LIB.csa_cache_read(
+        h.ptr, cache._ref, cu, p0, B, shape[0], _dtype(k_out), k, v, _stream_of(h, stream)))
+
+
+def csa_cache_attn_workspace(h: Handle, T_cap: int, H: int, H_kv: int, d: int) -> int:
+    return int(LIB.csa_cache_attn_workspace(h.ptr, int(T_cap), int(H), int(H_kv), int(d)))
+
+
+def csa_cache_attn_fwd(h: Handle, q, cu_seqlens, pos0, softmax_scale: float, out, ws, cmp=None, raw=None, idx=None,
+                       cu_cmp=None, ratio: int = 0, window: int = 0, sink=None, lse=None, stream=None):
+    """Attention of q [T_cap, H, d] over a cache of compressed entries (all visible ones, or
+    idx's) and the last ``window`` rows of a raw cache, in one softmax."""
+    if cmp is None and raw is None:
+        raise ValueError("neither cmp nor raw is given")
+    for c in (cmp, raw):
+        if c is not None:
+            B, cu, p0 = _packing(h, c, cu_seqlens, pos0)
+    T, H, d = q.shape
+    dev = h.device
+    ptr = [_want("q", q, q.dtype, (T, H, d), dev), _want("out", out, q.dtype, (T, H, d), dev)]
+    i = _want("idx", idx, torch.int32, (T, None), dev) if idx is not None else None
+    cc = _want("cu_cmp", cu_cmp, torch.int32, (B + 1,), dev) if cu_cmp is not None else None
+    sk = _want("sink", sink, torch.float32, (H,), dev) if sink is not None else None
+    ls = _want("lse", lse, torch.float32, (T, H), dev) if lse is not None else None
+    w = _want("ws", ws, ws.dtype, (None,), dev) if ws is not None else None
+    return _check("csa_cache_attn_fwd", LIB.csa_cache_attn_fwd(
+        h.ptr, ptr[0], cmp._ref if cmp is not None else None, raw._ref if raw is not None else None, i,
+        idx.shape[1] if idx is not None else 0, cc, sk, cu, p0, B, T, H, d, ratio, window, softmax_scale, _dtype(q),
+        ptr[1], ls, w, ws.numel() * ws.element_size() if ws is not None else 0, _stream_of(h, stream)))

@@ -22,6 +22,8 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 // Null or 16-byte aligned (optional arguments).
 bool opt_aligned16(const void* p) { return p == nullptr || aligned16(p); }
 
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
 csa_status_t from_cuda(cudaError_t e) { return e == cudaSuccess ? CSA_OK : CSA_ERR_CUDA; }
 
 bool pow2_in(int v, int lo, int hi) { return v >= lo && v <= hi && (v & (v - 1)) == 0; }
@@ -418,6 +420,99 @@ csa_status_t csa_indexer_topk_fp8(csa_handle_t h, const uint8_t* qI, const float
   return from_cuda(csa::launch_indexer_topk_fp8_full(qI, qI_scale, w, kI, kI_scale, cu, cu_cmp, B, T_cap, max_vis,
                                                      ratio, topk, k_pad, idx, h->status, stream, h->pos0,
                                                      h->cmp_rows));
+}
+
+namespace {
+
+// CSA_OK and the kernels' view of a cache, or why it is refused.
+csa_status_t cache_view(const csa_cache_t* c, csa::CacheView* out) {
+  if (!c || !c->k || !c->k_scale || !c->table || c->n_blocks < 0 || c->max_blocks < 0 || c->H_kv < 1)
+    return CSA_ERR_INVALID_ARG;
+  if ((c->v != nullptr) != (c->v_scale != nullptr)) return CSA_ERR_INVALID_ARG;
+  if (!aligned16(c->k) || !opt_aligned16(c->v) || !aligned4(c->k_scale) || !aligned4(c->v_scale) ||
+      !aligned4(c->table))
+    return CSA_ERR_INVALID_ARG;
+  if (!pow2_in(c->block, 16, 128) || (c->d != 64 && c->d != 128)) return CSA_ERR_UNSUPPORTED;
+  if ((int64_t)c->max_blocks * c->block > INT32_MAX || c->H_kv > 65535) return CSA_ERR_UNSUPPORTED;
+  int lg = 4;
+  while ((1 << lg) < c->block) ++lg;
+  *out = csa::CacheView{c->k, c->v, c->k_scale, c->v_scale, c->table, c->n_blocks, c->max_blocks,
+                        lg,   c->H_kv, c->d, c->max_blocks * c->block};
+  return CSA_OK;
+}
+
+bool dtype_ok(csa_dtype_t t) { return t == CSA_BF16 || t == CSA_FP32; }
+
+}  // namespace
+
+csa_status_t csa_cache_write(csa_handle_t h, const csa_cache_t* cache, const void* x_k, const void* x_v,
+                             const int32_t* cu, const int32_t* pos0, int B, int T_cap, csa_dtype_t dtype,
+                             cudaStream_t stream) {
+  if (!h || !packing_ok(cu, B, T_cap, 1) || !dtype_ok(dtype)) return CSA_ERR_INVALID_ARG;
+  csa::CacheView c;
+  const csa_status_t st = cache_view(cache, &c);
+  if (st != CSA_OK) return st;
+  if (B == 0 || T_cap == 0) return CSA_OK;  // no rows (empty arrays may have no address)
+  if (!x_k || !pos0 || (x_v != nullptr) != (c.v != nullptr) || !aligned16(x_k) || !opt_aligned16(x_v) || !aligned4(cu) ||
+      !aligned4(pos0))
+    return CSA_ERR_INVALID_ARG;
+  DeviceGuard g(h->device);
+  if (!g.ok) return CSA_ERR_CUDA;
+  return from_cuda(csa::launch_cache_write(c, x_k, x_v, cu, pos0, B, T_cap, dtype == CSA_FP32, h->status, stream));
+}
+
+csa_status_t csa_cache_read(csa_handle_t h, const csa_cache_t* cache, const int32_t* cu, const int32_t* pos0, int B,
+                            int T_cap, csa_dtype_t dtype, void* k_out, void* v_out, cudaStream_t stream) {
+  if (!h || !packing_ok(cu, B, T_cap, 1) || !dtype_ok(dtype)) return CSA_ERR_INVALID_ARG;
+  csa::CacheView c;
+  const csa_status_t st = cache_view(cache, &c);
+  if (st != CSA_OK) return st;
+  if (T_cap == 0) return CSA_OK;
+  if (!k_out || (B > 0 && !pos0) || (v_out != nullptr && c.v == nullptr) || !aligned16(k_out) || !opt_aligned16(v_out) || !aligned4(cu) ||
+      !aligned4(pos0))
+    return CSA_ERR_INVALID_ARG;
+  DeviceGuard g(h->device);
+  if (!g.ok) return CSA_ERR_CUDA;
+  return from_cuda(
+      csa::launch_cache_read(c, cu, pos0, B, T_cap, dtype == CSA_FP32, k_out, v_out, h->status, stream));
+}
+
+csa_status_t csa_cache_attn_fwd(csa_handle_t h, const void* q, const csa_cache_t* cmp, const csa_cache_t* raw,
+                                const int32_t* idx, int k_pad, const int32_t* cu_cmp, const float* sink,
+                                const int32_t* cu, const int32_t* pos0, int B, int T_cap, int H, int d, int ratio,
+                                int window, float softmax_scale, csa_dtype_t dtype, void* out, float* lse, void* ws,
+                                size_t ws_bytes, cudaStream_t stream) {
+  if (!h || !packing_ok(cu, B, T_cap, 1) || !dtype_ok(dtype) || (!cmp && !raw))
+    return CSA_ERR_INVALID_ARG;
+  if ((cmp && ratio < 1) || (raw && window < 1) || (idx && (!cmp || k_pad < 1)) || (cu_cmp && !idx) || H < 1 ||
+      (T_cap > 0 && (!q || !out || (B > 0 && !pos0))))
+    return CSA_ERR_INVALID_ARG;
+  csa::CacheAttnArgs a{};
+  csa_status_t st = CSA_OK;
+  if (cmp && (st = cache_view(cmp, &a.cmp)) != CSA_OK) return st;
+  if (raw && (st = cache_view(raw, &a.raw)) != CSA_OK) return st;
+  const csa::CacheView& c = cmp ? a.cmp : a.raw;
+  if (cmp && raw && (a.cmp.H_kv != a.raw.H_kv || a.cmp.d != a.raw.d || (a.cmp.v != nullptr) != (a.raw.v != nullptr)))
+    return CSA_ERR_INVALID_ARG;
+  if (c.d != d || H % c.H_kv != 0) return CSA_ERR_INVALID_ARG;
+  if (H / c.H_kv > 128) return CSA_ERR_UNSUPPORTED;
+  if (T_cap == 0) return CSA_OK;
+  if (!aligned16(q) || !aligned16(out) || !aligned4(lse) || !aligned4(sink) || !aligned4(idx) || !aligned4(cu_cmp) ||
+      !aligned4(cu) || !aligned4(pos0))
+    return CSA_ERR_INVALID_ARG;
+  const size_t need = csa_cache_attn_workspace(h, T_cap, H, c.H_kv, d);
+  if (need > 0 && (!ws || !aligned16(ws) || ws_bytes < need)) return CSA_ERR_WORKSPACE;
+  a.q = q; a.idx = idx; a.k_pad = k_pad; a.cu_cmp = cu_cmp; a.sink = sink; a.cu = cu; a.pos0 = pos0;
+  a.B = B; a.T_cap = T_cap; a.H = H; a.H_kv = c.H_kv; a.d = d; a.r = ratio; a.window = window;
+  a.scale = softmax_scale; a.out = out; a.lse = lse; a.ws = ws; a.status = h->status;
+  DeviceGuard g(h->device);
+  if (!g.ok) return CSA_ERR_CUDA;
+  return from_cuda(csa::launch_cache_attn(a, dtype == CSA_FP32, h->sm_count, stream));
+}
+
+size_t csa_cache_attn_workspace(csa_handle_t h, int T_cap, int H, int H_kv, int d) {
+  if (!h || T_cap < 0 || H < 1 || H_kv < 1 || H % H_kv != 0 || H / H_kv > 128 || (d != 64 && d != 128)) return 0;
+  return csa::cache_attn_workspace(h->sm_count, T_cap, H, H_kv, d);
 }
 
 }  // extern "C"

@@ -182,4 +182,40 @@ cudaError_t launch_indexer_kl_bwd_tc(const KLBwdArgs& a, cudaStream_t stream);
 bool indexer_kl_bwd_sparse_tc_supported(const KLBwdArgs& a, bool fp32);
 cudaError_t launch_indexer_kl_bwd_sparse_tc(const KLBwdArgs& a, cudaStream_t stream);
 
+// The 8-bit serving cache (csa_cache_t as the kernels take it).
+struct CacheView {
+  uint8_t* k;
+  uint8_t* v;
+  float* k_scale;
+  float* v_scale;
+  const int32_t* table;
+  int n_blocks, max_blocks;
+  int log_block;        // block = 1 << log_block rows
+  int H_kv, d;
+  int cap;              // max_blocks * block: rows a table can name
+};
+cudaError_t launch_cache_write(const CacheView& c, const void* x_k, const void* x_v, const int32_t* cu,
+                               const int32_t* pos0, int B, int T_cap, bool fp32, int* status, cudaStream_t stream);
+cudaError_t launch_cache_read(const CacheView& c, const int32_t* cu, const int32_t* pos0, int B, int T_cap, bool fp32,
+                              void* k_out, void* v_out, int* status, cudaStream_t stream);
+
+struct CacheAttnArgs {
+  const void* q;
+  CacheView cmp, raw;    // k == nullptr: absent
+  const int32_t* idx;
+  int k_pad;
+  const int32_t* cu_cmp; // optional: idx holds global compressed rows
+  const float* sink;
+  const int32_t* cu;
+  const int32_t* pos0;
+  int B, T_cap, H, H_kv, d, r, window;
+  float scale;
+  void* out;
+  float* lse;
+  void* ws;
+  int* status;
+};
+size_t cache_attn_workspace(int sm_count, int T_cap, int H, int H_kv, int d);
+cudaError_t launch_cache_attn(const CacheAttnArgs& a, bool fp32, int sm_count, cudaStream_t stream);
+
 }  // namespace csa

@@ -432,6 +432,97 @@ csa_status_t csa_indexer_kl_bwd(csa_handle_t handle, const void* q, const void* 
                                 float grad_scale, csa_dtype_t dtype, void* dqI, void* dw,
                                 float* dkI, cudaStream_t stream);
 
+/* ---- Serving: a paged cache in 8 bits -----------------------------------
+ * One decode step of the layers above: the new rows are written into caches
+ * held in E4M3, and the new queries attend to the cached compressed entries
+ * and raw rows.  A cache holds rows of H_kv heads x d dims in blocks of
+ * `block` consecutive rows; row `pos` of sequence b is row pos % block of
+ * block table[b][pos / block].  Codes of one block and head are contiguous,
+ * with one power-of-two scale: value = code * scale.
+ * The struct is read on the host during the call; the arrays are the
+ * caller's (16-byte aligned; tables and scales 4-byte aligned).  Blocks may
+ * appear in several tables (a shared prefix); table entries that a call does
+ * not reach may hold anything. */
+typedef struct csa_cache_s {
+  uint8_t* k;            /* [n_blocks, H_kv, block, d] E4M3 codes */
+  uint8_t* v;            /* the same, or NULL: V = K */
+  float* k_scale;        /* [n_blocks, H_kv] */
+  float* v_scale;        /* the same, set exactly when v is */
+  const int32_t* table;  /* [B, max_blocks] block numbers, 0 .. n_blocks - 1 */
+  int n_blocks, max_blocks;
+  int block;             /* rows of a block: 16, 32, 64 or 128 */
+  int H_kv, d;           /* d 64 or 128 */
+} csa_cache_t;
+
+/* Quantise rows into a cache as they arrive.  Packed row cu_seqlens[b] + i of
+ * x_k (and x_v, given exactly when the cache has V) [T_cap, H_kv, d] (dtype)
+ * becomes row pos0[b] + i of sequence b (pos0 [B] int32, device).
+ * Scale of a block and head: the smallest s = 2^e with e >= -126 and
+ * max|x| / s <= 448 over the finite elements written to it since its first
+ * row was (2^-126 when they are all zero).  Rows that join a block behind
+ * earlier ones keep its scale unless they need a larger one; the codes of
+ * the earlier rows are then rescaled (exact except where codes fall below
+ * E4M3's normal range: rounded to nearest even once more).  A block whose
+ * first row is written takes a new scale.  code = E4M3(x / s), rounded to
+ * nearest even; infinities and NaN become NaN.  float32 rows are quantised
+ * as they are.  Rows behind the last one written keep their codes (they mean
+ * nothing under a new scale).  Capacity rows are not read.
+ * Only one sequence may write to a block in one call.  A sequence whose
+ * positions are negative or reach past max_blocks * block, and a block number
+ * out of range, raise CSA_ERR_DEVICE_BOUNDS and are skipped.
+ * H_kv >= 1; other block, d: CSA_ERR_UNSUPPORTED. */
+csa_status_t csa_cache_write(csa_handle_t handle, const csa_cache_t* cache, const void* x_k,
+                             const void* x_v, const int32_t* cu_seqlens, const int32_t* pos0,
+                             int B, int T_cap, csa_dtype_t dtype, cudaStream_t stream);
+
+/* Read rows back: k_out (and v_out, if given) [T_cap, H_kv, d] (dtype), row
+ * cu_seqlens[b] + i = code * scale of row pos0[b] + i of sequence b, rounded
+ * once to bf16 (exact in float32).  v_out must be NULL when V = K.  Capacity
+ * rows and skipped rows are written as zeros.  Errors as csa_cache_write. */
+csa_status_t csa_cache_read(csa_handle_t handle, const csa_cache_t* cache,
+                            const int32_t* cu_seqlens, const int32_t* pos0, int B, int T_cap,
+                            csa_dtype_t dtype, void* k_out, void* v_out, cudaStream_t stream);
+
+/* Attention of new query rows over cached compressed entries and cached raw
+ * rows in one softmax: the serving form of csa_sparse_attn_fwd, hca_attn_fwd
+ * and window_attn_fwd, with grouped KV heads.  Query row cu_seqlens[b] + i has
+ * position p = pos0[b] + i in its sequence; its candidates are
+ *   cmp (may be NULL):  entries j with ratio (j + 1) - 1 <= p of sequence b's
+ *     compressed cache -- every one (idx NULL), or those that idx[t, 0..k_pad)
+ *     lists: global compressed rows cu_cmp[b] + j as csa_indexer_topk writes
+ *     them, or plain entries j when cu_cmp is NULL; -1 is skipped, an entry
+ *     listed twice counts twice.  ratio 1 is causal attention over a cache.
+ *   raw (may be NULL):  rows [max(0, p - window + 1), p] of sequence b's raw
+ *     cache; the new rows themselves are written before this call.
+ * Query head h reads KV head h / (H / H_kv).  With s_i = softmax_scale q.K_i,
+ *   out[t,h,:] = sum_i softmax_i(s_i; sink_h) V_i,  lse[t,h] = log(sum_i e^{s_i} + e^{sink_h})
+ * Rows without a candidate: out = 0, lse = sink_h (-inf without a sink).
+ * Capacity rows: out = 0, lse = -inf.
+ *   q, out [T_cap, H, d] (dtype);  lse [T_cap, H] float32 or NULL;  sink [H] float32 or NULL
+ * The scores, the softmax and the sums are float32 on exact cached values;
+ * bf16 queries are exact too and the weights enter the value products in 11
+ * bits; float32 queries and weights enter the products in 22 bits.
+ * ws: device scratch of csa_cache_attn_workspace bytes, 16-byte aligned, any
+ * contents; calls that may overlap on the GPU need one each.  Results do not
+ * depend on what is in it and are the same from run to run.
+ * Both caches, when given, have the same H_kv, d and V; H a multiple of H_kv
+ * with H / H_kv <= 128.  At least one cache; window >= 1 with raw, ratio >= 1
+ * with cmp; idx only with cmp.  A sequence whose positions are negative or
+ * reach past a cache's max_blocks * block, an idx entry outside a query's
+ * visible entries and a block number out of range raise
+ * CSA_ERR_DEVICE_BOUNDS; the entries (the whole sequence) count as absent. */
+csa_status_t csa_cache_attn_fwd(csa_handle_t handle, const void* q, const csa_cache_t* cmp,
+                                const csa_cache_t* raw, const int32_t* idx, int k_pad,
+                                const int32_t* cu_cmp, const float* sink,
+                                const int32_t* cu_seqlens, const int32_t* pos0, int B, int T_cap,
+                                int H, int d, int ratio, int window, float softmax_scale,
+                                csa_dtype_t dtype, void* out, float* lse, void* ws,
+                                size_t ws_bytes, cudaStream_t stream);
+
+/* Scratch bytes csa_cache_attn_fwd needs (it does not depend on the caches'
+ * lengths); 0 for a null handle or a shape it refuses. */
+size_t csa_cache_attn_workspace(csa_handle_t handle, int T_cap, int H, int H_kv, int d);
+
 #ifdef __cplusplus
 }
 #endif
