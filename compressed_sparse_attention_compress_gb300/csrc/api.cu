@@ -433,7 +433,8 @@ csa_status_t cache_view(const csa_cache_t* c, csa::CacheView* out) {
       !aligned4(c->table))
     return CSA_ERR_INVALID_ARG;
   if (!pow2_in(c->block, 16, 128) || (c->d != 64 && c->d != 128)) return CSA_ERR_UNSUPPORTED;
-  if ((int64_t)c->max_blocks * c->block > INT32_MAX || c->H_kv > 65535) return CSA_ERR_UNSUPPORTED;
+  if ((int64_t)c->max_blocks * c->block > (1 << 30) || (int64_t)c->n_blocks * c->H_kv > INT32_MAX)
+    return CSA_ERR_UNSUPPORTED;
   int lg = 4;
   while ((1 << lg) < c->block) ++lg;
   *out = csa::CacheView{c->k, c->v, c->k_scale, c->v_scale, c->table, c->n_blocks, c->max_blocks,
@@ -495,7 +496,7 @@ csa_status_t csa_cache_attn_fwd(csa_handle_t h, const void* q, const csa_cache_t
   if (cmp && raw && (a.cmp.H_kv != a.raw.H_kv || a.cmp.d != a.raw.d || (a.cmp.v != nullptr) != (a.raw.v != nullptr)))
     return CSA_ERR_INVALID_ARG;
   if (c.d != d || H % c.H_kv != 0) return CSA_ERR_INVALID_ARG;
-  if (H / c.H_kv > 128) return CSA_ERR_UNSUPPORTED;
+  if (H / c.H_kv > 128 || (int64_t)T_cap * H > INT32_MAX || (int64_t)T_cap + B > INT32_MAX) return CSA_ERR_UNSUPPORTED;
   if (T_cap == 0) return CSA_OK;
   if (!aligned16(q) || !aligned16(out) || !aligned4(lse) || !aligned4(sink) || !aligned4(idx) || !aligned4(cu_cmp) ||
       !aligned4(cu) || !aligned4(pos0))
