@@ -433,7 +433,8 @@ csa_status_t cache_view(const csa_cache_t* c, csa::CacheView* out) {
       !aligned4(c->table))
     return CSA_ERR_INVALID_ARG;
   if (!pow2_in(c->block, 16, 128) || (c->d != 64 && c->d != 128)) return CSA_ERR_UNSUPPORTED;
-  if ((int64_t)c->max_blocks * c->block > (1 << 30) || (int64_t)c->n_blocks * c->H_kv > INT32_MAX)
+  if ((int64_t)c->max_blocks * c->block > (1 << 30) || (int64_t)c->n_blocks * c->H_kv > INT32_MAX ||
+      (int64_t)c->n_blocks * c->H_kv * c->block > UINT32_MAX - 1)
     return CSA_ERR_UNSUPPORTED;
   int lg = 4;
   while ((1 << lg) < c->block) ++lg;
@@ -504,7 +505,9 @@ csa_status_t csa_cache_attn_fwd(csa_handle_t h, const void* q, const csa_cache_t
   const size_t need = csa_cache_attn_workspace(h, T_cap, H, c.H_kv, d);
   if (need > 0 && (!ws || !aligned16(ws) || ws_bytes < need)) return CSA_ERR_WORKSPACE;
   a.q = q; a.idx = idx; a.k_pad = k_pad; a.cu_cmp = cu_cmp; a.sink = sink; a.cu = cu; a.pos0 = pos0;
-  a.B = B; a.T_cap = T_cap; a.H = H; a.H_kv = c.H_kv; a.d = d; a.r = ratio; a.window = window;
+  a.B = B; a.T_cap = T_cap; a.H = H; a.H_kv = c.H_kv; a.d = d; a.r = ratio;
+  a.window = window < (1 << 30) ? window : 1 << 30;  // no cache is longer
+ 
   a.scale = softmax_scale; a.out = out; a.lse = lse; a.ws = ws; a.status = h->status;
   DeviceGuard g(h->device);
   if (!g.ok) return CSA_ERR_CUDA;

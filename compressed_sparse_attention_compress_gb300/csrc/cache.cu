@@ -19,54 +19,81 @@ namespace csa {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kKeep = 8;  // 8-element chunks a thread holds between the two passes
+constexpr int kKeep = 4;  // 8-element chunks that a thread holds between the two passes
 
-// Eight consecutive elements as float32.
-template <typename T> __device__ __forceinline__ void load8(const T* p, float (&v)[8]);
-template <> __device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* p, float (&v)[8]) {
-  const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+// Eight consecutive elements, as they are stored.
+template <typename T> struct Chunk;
+template <> struct Chunk<__nv_bfloat16> {
+  uint4 u;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = __ldg(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) v[2 * i] = bf16_lo(w[i]), v[2 * i + 1] = bf16_hi(w[i]);
-}
-template <> __device__ __forceinline__ void load8<float>(const float* p, float (&v)[8]) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const float4 f = __ldg(reinterpret_cast<const float4*>(p) + i);
-    v[4 * i] = f.x, v[4 * i + 1] = f.y, v[4 * i + 2] = f.z, v[4 * i + 3] = f.w;
+    for (int i = 0; i < 4; ++i) v[2 * i] = bf16_lo(w[i]), v[2 * i + 1] = bf16_hi(w[i]);
   }
-}
+};
+template <> struct Chunk<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = __ldg(reinterpret_cast<const float4*>(p));
+    b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  }
+};
 
 // First slot of sequence b: consecutive sequences are at least as far apart as
 // the blocks that the earlier one's rows can touch.
-__device__ __forceinline__ int64_t slot_base(const int32_t* cu, int b, int lg) {
-  return ((int64_t)__ldg(cu + b) >> lg) + 2 * (int64_t)b;
+__device__ __forceinline__ int64_t slot_base(int32_t cu, int b, int lg) {
+  return ((int64_t)cu >> lg) + 2 * (int64_t)b;
 }
 
-// The last b with slot_base(b) <= slot, searched by a whole warp, 32 ways a step.
-__device__ __forceinline__ int slot_owner(const int32_t* cu, int B, int lg, int64_t slot, int lane) {
-  int lo = 0, n = B;
-  while (true) {
-    const int step = (n + 31) / 32;
-    const int at = lane * step;
-    const bool le = at < n && slot_base(cu, lo + at, lg) <= slot;
-    const int c = __popc(__ballot_sync(0xffffffffu, le));
-    const int skip = max(c - 1, 0) * step;
-    lo += skip;
-    n = min(step, n - skip);
-    if (n <= 1) return lo;
+struct Owner {
+  int b, row0, row1, p0;
+  int64_t base;
+};
+
+// The last sequence b with slot_base <= slot, by a whole warp: one round of
+// loads up to 31 sequences, 32 ways a round above.
+__device__ __forceinline__ Owner slot_owner(const int32_t* cu, const int32_t* pos0, int B, int lg, int64_t slot,
+                                            int lane) {
+  Owner o;
+  if (B < 32) {
+    const int cv = lane <= B ? __ldg(cu + lane) : 0, pv = lane < B ? __ldg(pos0 + lane) : 0;
+    o.b = max(__popc(__ballot_sync(0xffffffffu, lane < B && slot_base(cv, lane, lg) <= slot)) - 1, 0);
+    o.row0 = __shfl_sync(0xffffffffu, cv, o.b);
+    o.row1 = __shfl_sync(0xffffffffu, cv, o.b + 1);
+    o.p0 = __shfl_sync(0xffffffffu, pv, o.b);
+  } else {
+    int lo = 0, n = B;
+    while (n > 1) {
+      const int step = (n + 31) / 32, at = lane * step;
+      const bool le = at < n && slot_base(__ldg(cu + lo + at), lo + at, lg) <= slot;
+      const int skip = max(__popc(__ballot_sync(0xffffffffu, le)) - 1, 0) * step;
+      lo += skip;
+      n = min(step, n - skip);
+    }
+    o.b = lo;
+    o.row0 = __ldg(cu + lo);
+    o.row1 = __ldg(cu + lo + 1);
+    o.p0 = __ldg(pos0 + lo);
   }
+  o.base = slot_base(o.row0, o.b, lg);
+  return o;
 }
 
-template <typename T, int D, int TPI>  // TPI: threads of an item
-__global__ void __launch_bounds__(kThreads)
+// kWarpItems: a warp per item, 8 items a CTA (few rows per sequence); else a CTA
+// per item, whose threads hold kKeep chunks each of a full block.
+template <typename T, int D, bool kWarpItems>
+__global__ void __launch_bounds__(kWarpItems ? kThreads : 512)
 cache_write_kernel(CacheView c, const T* __restrict__ x_k, const T* __restrict__ x_v, const int32_t* __restrict__ cu,
                    const int32_t* __restrict__ pos0, int B, int T_cap, int64_t n_items, int* status) {
   constexpr int kChunks = D / 8;
-  __shared__ float s_max[kThreads / 32];
+  __shared__ float s_max[16];
   const int lane = threadIdx.x & 31;
-  const int t = threadIdx.x % TPI;
-  const int64_t item = (int64_t)blockIdx.x * (kThreads / TPI) + threadIdx.x / TPI;
+  const int t = kWarpItems ? lane : threadIdx.x, n_t = kWarpItems ? 32 : blockDim.x;
+  const int64_t item = kWarpItems ? (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5) : blockIdx.x;
   if (item >= n_items) return;
   const int kinds = c.v ? 2 : 1;
   const int h = (int)(item % c.H_kv);
@@ -74,58 +101,57 @@ cache_write_kernel(CacheView c, const T* __restrict__ x_k, const T* __restrict__
   const int64_t slot = item / (c.H_kv * kinds);
   const int lg = c.log_block, P = 1 << lg;
 
-  const int b = slot_owner(cu, B, lg, slot, lane);
-  const int row0 = __ldg(cu + b), L = __ldg(cu + b + 1) - row0;
-  const int p0 = __ldg(pos0 + b);
+  const Owner o = slot_owner(cu, pos0, B, lg, slot, lane);
+  const int row0 = o.row0, L = o.row1 - row0, p0 = o.p0;
   if (L <= 0 || row0 < 0 || (int64_t)row0 + L > T_cap) return;
   if (p0 < 0 || (int64_t)p0 + L > c.cap) {
     if (t == 0) raise_status(status, CSA_ERR_DEVICE_BOUNDS);
     return;
   }
-  const int64_t nth = slot - slot_base(cu, b, lg);
+  const int64_t nth = slot - o.base;
   const int64_t j = (p0 >> lg) + nth;  // block of the sequence
   if (nth < 0 || (j << lg) >= (int64_t)p0 + L) return;
-  const int first = (int)(j << lg);                              // position of the block's first row
+  const int first = (int)(j << lg);  // position of the block's first row
   const int lo = max(p0 - first, 0), hi = min(p0 + L - first, P);
-  const int blk = cache_block(c, b, first, status);
-  if (blk < 0) return;
-
+  const int n = (hi - lo) * kChunks;
   const T* x = (is_v ? x_v : x_k) + (((int64_t)row0 + first + lo - p0) * c.H_kv + h) * D;
   const int64_t stride = (int64_t)c.H_kv * D;
-  uint8_t* codes = (is_v ? c.v : c.k) + ((int64_t)blk * c.H_kv + h) * ((int64_t)P * D);
-  float* scale = (is_v ? c.v_scale : c.k_scale) + (int64_t)blk * c.H_kv + h;
-  const float old_s = lo > 0 ? *scale : 0.f;
-  const int n = (hi - lo) * kChunks;
 
-  float v[kKeep][8];
-  float amax = 0.f;
+  Chunk<T> v[kKeep];
   auto load = [&](int base) {
 #pragma unroll
     for (int k = 0; k < kKeep; ++k) {
-      const int i = base + t + k * TPI;
-      if (i < n) load8(x + (i / kChunks) * stride + (i % kChunks) * 8, v[k]);
+      const int i = base + t + k * n_t;
+      if (i < n) v[k].load(x + (i / kChunks) * stride + (i % kChunks) * 8);
     }
   };
-  for (int base = 0; base < n; base += TPI * kKeep) {
-    load(base);
+  load(0);
+  const int blk = cache_block(c, o.b, first, status);
+  if (blk < 0) return;
+  uint8_t* codes = (is_v ? c.v : c.k) + ((int64_t)blk * c.H_kv + h) * ((int64_t)P * D);
+  float* scale = (is_v ? c.v_scale : c.k_scale) + (int64_t)blk * c.H_kv + h;
+  const float old_s = lo > 0 ? *scale : 0.f;
+
+  float amax = 0.f;
+  for (int base = 0; base < n; base += n_t * kKeep) {
+    if (base > 0) load(base);
 #pragma unroll
     for (int k = 0; k < kKeep; ++k) {
-      if (base + t + k * TPI < n) {
+      if (base + t + k * n_t < n) {
+        float f[8];
+        v[k].get(f);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float a = fabsf(v[k][e]);
-          if (a < INFINITY) amax = fmaxf(amax, a);
-        }
+        for (int e = 0; e < 8; ++e)
+          if (fabsf(f[e]) < INFINITY) amax = fmaxf(amax, fabsf(f[e]));
       }
     }
   }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  if (TPI > 32) {
+  for (int s = 16; s > 0; s >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, s));
+  if (!kWarpItems) {
     if (lane == 0) s_max[threadIdx.x >> 5] = amax;
     __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) amax = fmaxf(amax, s_max[w]);
+    for (int w = 0; w < (n_t >> 5); ++w) amax = fmaxf(amax, s_max[w]);
   }
   const float need = pow2i(e4m3_scale_exponent(amax));
   const float new_s = lo > 0 ? fmaxf(old_s, need) : need;
@@ -133,7 +159,7 @@ cache_write_kernel(CacheView c, const T* __restrict__ x_k, const T* __restrict__
   if (lo > 0 && new_s > old_s) {  // the codes before the new rows, under the larger scale
     const float f = old_s / new_s;
     uint4* row = reinterpret_cast<uint4*>(codes);
-    for (int i = t; i < lo * (D / 16); i += TPI) {
+    for (int i = t; i < lo * (D / 16); i += n_t) {
       uint4 u = row[i];
       uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -147,24 +173,19 @@ cache_write_kernel(CacheView c, const T* __restrict__ x_k, const T* __restrict__
     }
   }
   const float inv = 1.f / new_s;  // a power of two
-  for (int base = 0; base < n; base += TPI * kKeep) {
-    if (n > TPI * kKeep) load(base);  // more rows than the registers held
+  for (int base = 0; base < n; base += n_t * kKeep) {
+    if (n > n_t * kKeep) load(base);  // more rows than the registers held
 #pragma unroll
     for (int k = 0; k < kKeep; ++k) {
-      const int i = base + t + k * TPI;
+      const int i = base + t + k * n_t;
       if (i < n) {
-        uint32_t w[2];
+        float f[8];
+        v[k].get(f);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float y[4];
-#pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            const float a = v[k][4 * e + g];
-            y[g] = fabsf(a) < INFINITY ? a * inv : NAN;
-          }
-          w[e] = (uint32_t)e4m3x2_from_floats(y[0], y[1]) | (uint32_t)e4m3x2_from_floats(y[2], y[3]) << 16;
-        }
-        *reinterpret_cast<uint2*>(codes + (lo + i / kChunks) * D + (i % kChunks) * 8) = make_uint2(w[0], w[1]);
+        for (int e = 0; e < 8; ++e) f[e] = fabsf(f[e]) < INFINITY ? f[e] * inv : NAN;
+        const uint32_t w0 = (uint32_t)e4m3x2_from_floats(f[0], f[1]) | (uint32_t)e4m3x2_from_floats(f[2], f[3]) << 16;
+        const uint32_t w1 = (uint32_t)e4m3x2_from_floats(f[4], f[5]) | (uint32_t)e4m3x2_from_floats(f[6], f[7]) << 16;
+        *reinterpret_cast<uint2*>(codes + (lo + i / kChunks) * D + (i % kChunks) * 8) = make_uint2(w0, w1);
       }
     }
   }
@@ -247,11 +268,11 @@ void write_launch(const CacheView& c, const void* x_k, const void* x_v, const in
   const T* k = static_cast<const T*>(x_k);
   const T* v = static_cast<const T*>(x_v);
   if (T_cap <= 4 * (int64_t)B)
-    cache_write_kernel<T, D, 32><<<(unsigned)((items + 7) / 8), kThreads, 0, stream>>>(c, k, v, cu, pos0, B, T_cap,
-                                                                                      items, status);
+    cache_write_kernel<T, D, true><<<(unsigned)((items + 7) / 8), kThreads, 0, stream>>>(c, k, v, cu, pos0, B, T_cap,
+                                                                                        items, status);
   else
-    cache_write_kernel<T, D, kThreads><<<(unsigned)items, kThreads, 0, stream>>>(c, k, v, cu, pos0, B, T_cap, items,
-                                                                                status);
+    cache_write_kernel<T, D, false><<<(unsigned)items, (D / 8 << c.log_block) / kKeep, 0, stream>>>(
+        c, k, v, cu, pos0, B, T_cap, items, status);
 }
 
 template <typename T, int D>

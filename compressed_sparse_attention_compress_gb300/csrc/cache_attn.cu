@@ -38,9 +38,13 @@ using ws::ex2;
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kStep = 16;              // keys of a warp's step
+constexpr int kStep = 32;              // keys of a warp's step
 constexpr int kTile = kStep * kWarps;  // keys of a tile
-constexpr int kSeqSmem = 1024;         // so many sequences' offsets are kept in shared memory
+constexpr int kAhead = 4;              // steps whose rows are looked up together
+constexpr float kBase = 7.f;           // largest weight in the products when M is exact: 2^kBase ...
+constexpr float kSlack = 8.f;          // ... and M may lag by this much (a half ends below 2^16)
+constexpr float kNone = -3e38f;        // M before the first key
+constexpr uint32_t kNoRow = 0xffffffffu;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint4& a, uint32_t b0, uint32_t b1) {
@@ -60,11 +64,13 @@ __device__ __forceinline__ uint32_t rest_f16x2(uint32_t hi, float a, float b) {
 }
 __device__ __forceinline__ uint32_t widen_lo(uint32_t w) { return e4m3x2_to_f16x2((uint16_t)w); }
 __device__ __forceinline__ uint32_t widen_hi(uint32_t w) { return e4m3x2_to_f16x2((uint16_t)(w >> 16)); }
-__device__ __forceinline__ float2 lds_f2(uint32_t a) {
-  float2 v;
-  asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a));
+__device__ __forceinline__ float lds_f(uint32_t a) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a));
   return v;
 }
+// Exponent of a power of two.
+__device__ __forceinline__ float exponent_of(float s) { return (float)((int)(__float_as_uint(s) >> 23) - 127); }
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 v;
   asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
@@ -82,6 +88,12 @@ __device__ __forceinline__ void cp_async_4_zfill(uint32_t dst, const void* src, 
 // Any NaN code (0x7f with either sign) among four.
 __device__ __forceinline__ bool has_nan4(uint32_t w) { return (((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0; }
 
+// The same codes, NaN as 0.
+__device__ __forceinline__ uint32_t without_nan4(uint32_t w) {
+  const uint32_t nan = ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+  return w & ~(nan | (nan - (nan >> 7)));
+}
+
 // Byte offset of 16-byte chunk `ch` of row `row` in a 16-row tile of codes.  The
 // chunks of a 128-byte line are permuted so that the eight lanes of a 16-byte
 // read phase hit all banks: K reads take four chunks of two neighbouring rows,
@@ -90,6 +102,24 @@ template <int D> __device__ __forceinline__ int code_offset(int row, int ch) {
   if (D == 128) return row * 128 + ((ch ^ (((row >> 1) & 1) << 1 | (((row >> 2) ^ row) & 1) << 2)) << 4);
   const int line = row >> 1;
   return line * 128 + ((((row & 1) * 4 + ch) ^ ((line & 3) << 1)) << 4);
+}
+
+// Notes the dims in which rows r see a NaN among the 16 V rows at `at` (half hf of a
+// step whose first key is `first`): rare, so small rather than fast.
+template <int D, int R>
+__device__ __noinline__ void note_nans(uint32_t at, int hf, int first, bool entries, int window, const int* s_p,
+                                       const int* s_vis, uint32_t* s_nan, int lane) {
+  for (int i = lane; i < 16 * D; i += 32) {
+    const int key = 16 * hf + i / D, d = i % D;
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(at + code_offset<D>(key, d / 16) + d % 16));
+    if ((v & 0x7f) != 0x7f) continue;
+    const int pos = first + key;
+    for (int r = 0; r < R; ++r)
+      if (entries ? pos < s_vis[r] : pos <= s_p[r] && pos > s_p[r] - window)
+        atomicOr(s_nan + (r * D + d) / 32, 1u << (d % 32));
+  }
+  __syncwarp();
 }
 
 struct Plan {  // what every CTA derives from the arguments
@@ -135,7 +165,7 @@ __device__ __forceinline__ Slot find_slot(const CacheAttnArgs& a, const Plan& pl
     r.ct = (r.vis + kTile - 1) / kTile;
   }
   if (a.raw.k) {
-    r.w0 = max(0, r.p0 - a.window + 1) & ~(kStep - 1);  // a step's 16 keys lie in one block
+    r.w0 = max(0, r.p0 - a.window + 1) & ~15;  // 16 keys lie in one block
     r.rt = (p1 - r.w0) / kTile + 1;
   }
   if (r.ct + r.rt == 0) r.ct = 1;  // nothing in sight: the rows are still written
@@ -144,16 +174,17 @@ __device__ __forceinline__ Slot find_slot(const CacheAttnArgs& a, const Plan& pl
 
 template <int D, int MT, bool kSplit, bool kShared> struct Layout {
   static constexpr int R = 16 * MT;
-  static constexpr int kCodes = kStep * D;                                   // bytes of 16 rows
+  static constexpr int kCodes = kStep * D;                                   // bytes of a step's rows
   static constexpr int kStage = kCodes * (kShared ? 1 : 2) + 2 * kStep * 4;  // K, V, their scales
-  // copies of kStages - 1 steps are in flight: 96 KB an SM at 128 dims with separate V
-  static constexpr int kStages = D == 128 && !kShared && MT == 1 ? 3 : 4;
+  // copies of kStages - 1 steps are in flight: 96 KB an SM at 128 dims with separate V and three CTAs
+  static constexpr int kStages = D == 128 && !kShared ? 2 : 4;
   static constexpr int kRing = kStages * kStage * kWarps;
   static constexpr int kMerge = kWarps * R * D * 4;
-  static constexpr int kBuf = kRing > kMerge ? kRing : kMerge;
+  static constexpr int kSums = 3 * kWarps * R * 4;                           // each warp's m, M, l behind them
+  static constexpr int kBuf = kRing > kMerge + kSums ? kRing : kMerge + kSums;
   static constexpr int kQ = MT * (D / 16) * 32 * 16 * (kSplit ? 2 : 1);      // query fragments
-  static constexpr int kSmem = kBuf + kQ;
-  static constexpr bool kQRegs = MT == 1 && !kSplit;                         // fragments held in registers
+  static constexpr int kRows = kBuf + kQ;                                    // rows of the next steps
+  static constexpr int kSmem = kRows + kWarps * 2 * kAhead * kStep * 4;      // three CTAs an SM fit with MT = 1
 };
 
 // One piece of an item in the workspace: O [R][D], then m, M, l [R].
@@ -164,14 +195,12 @@ template <typename T, int D>
 __device__ __forceinline__ void finish_row(const CacheAttnArgs& a, int at, int d4, float4 v, float m, float M, float l) {
   if (a.sink) {  // it joins the sum and has no value row
     const float s2 = __ldg(a.sink + at % a.H) * kLog2e, top = fmaxf(m, s2);
-    if (top > -INFINITY) {
-      l = (m == -INFINITY ? l : l * ex2(m - top)) + ex2(s2 - top);
-      m = top;
-    }
+    l = l * ex2(m - top) + (s2 > kNone ? ex2(s2 - top) : 0.f);
+    m = top;
   }
-  if (M == -INFINITY && l == l) v = make_float4(0.f, 0.f, 0.f, 0.f);  // no key in sight
+  if (M == kNone && l == l) v = make_float4(0.f, 0.f, 0.f, 0.f);  // no key in sight
   else {
-    const float f = ex2(0.5f * (M - 15.f - m)), f2 = f / l;           // 2^(M - 15 - m) in two halves
+    const float f = ex2(0.5f * (M - kBase - m)), f2 = f / l;          // 2^(M - kBase - m) in two halves
     v.x = v.x * f * f2, v.y = v.y * f * f2, v.z = v.z * f * f2, v.w = v.w * f * f2;
   }
   T* out = static_cast<T*>(a.out) + (int64_t)at * D + 4 * d4;
@@ -182,19 +211,20 @@ __device__ __forceinline__ void finish_row(const CacheAttnArgs& a, int at, int d
 
 template <typename T, int D, int MT, bool kShared>
 __global__ void __launch_bounds__(kThreads, MT == 1 ? 3 : 2)
-cache_attn_kernel(const CacheAttnArgs a, const Plan pl, float* __restrict__ ws_o, int4* __restrict__ ws_meta) {
+cache_attn_kernel(const CacheAttnArgs a, const Plan pl, float* __restrict__ ws_o, int4* __restrict__ ws_meta,
+                  float* ws_far) {
   constexpr bool kSplit = sizeof(T) == 4;
   using L = Layout<D, MT, kSplit, kShared>;
   constexpr int R = L::R, kStages = L::kStages;
-  extern __shared__ __align__(1024) uint8_t smem[];
-  __shared__ int s_cu[kSeqSmem + 1], s_pos[kSeqSmem];
+  extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int64_t s_sum[kWarps];
   __shared__ int64_t s_at;
   __shared__ int s_slot;
   __shared__ float s_qf[R];                       // a row's query is q * 2^-e; 2^e
-  __shared__ int s_p[R];                          // a row's position, -1: no such row
+  __shared__ int s_p[R], s_vis[R];                // a row's position (-1: no such row), the entries that it sees
+  __shared__ uint32_t s_nan[R * D / 32];          // dims of a row that a NaN reached (see note_nans)
+  __shared__ int s_nans;
   __shared__ int s_out[R];                        // and its place: packed row * H + head
-  __shared__ float s_m[kWarps][R], s_M[kWarps][R], s_l[kWarps][R];
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, c = lane & 3;
@@ -205,14 +235,15 @@ cache_attn_kernel(const CacheAttnArgs a, const Plan pl, float* __restrict__ ws_o
   // ---- this CTA's share of the tiles ----
   const int32_t* cu = a.cu;
   const int32_t* pos0 = a.pos0;
-  if (a.B <= kSeqSmem) {
+  if ((2 * (int64_t)a.B + 1) * 4 <= L::kBuf) {  // searched by every thread: where the rings will be
+    int32_t* s_cu = reinterpret_cast<int32_t*>(smem);
     for (int i = tid; i <= a.B; i += kThreads) {
       s_cu[i] = __ldg(a.cu + i);
-      if (i < a.B) s_pos[i] = __ldg(a.pos0 + i);
+      if (i < a.B) s_cu[a.B + 1 + i] = __ldg(a.pos0 + i);
     }
     __syncthreads();
     cu = s_cu;
-    pos0 = s_pos;
+    pos0 = s_cu + a.B + 1;
   }
   const int n_slots = a.B > 0 ? pl.slots : 0;
   const int per = (n_slots + kThreads - 1) / kThreads;
@@ -271,6 +302,7 @@ cache_attn_kernel(const CacheAttnArgs a, const Plan pl, float* __restrict__ ws_o
   }
 
   const uint32_t ring = buf + warp * (kStages * L::kStage);
+  uint32_t* rows = reinterpret_cast<uint32_t*>(smem + L::kRows) + warp * (2 * kAhead * kStep);
   // lane constants of the fragment reads
   int off_k[D / 64], off_v[2];
 #pragma unroll
@@ -278,13 +310,16 @@ cache_attn_kernel(const CacheAttnArgs a, const Plan pl, float* __restrict__ ws_o
 #pragma unroll
   for (int e = 0; e < 2; ++e)
     off_v[e] = D == 128 ? code_offset<D>(2 * c + e, g) : code_offset<D>(2 * c + e, g >> 1) + (g & 1) * 8;
+  float* far_m = ws_far + ((int64_t)blockIdx.x * kWarps + warp) * (2 * R);  // log2 maximum and sum of far steps
+  float* far_l = far_m + R;
+  const float scale_log2 = fabsf(a.scale) * kLog2e;  // its sign is put into the queries
 
   int64_t u = u0;
   int slot = u0 < u1 ? s_slot : 0;
   int64_t slot_at = u0 < u1 ? s_at : 0;
   while (u < u1) {
     // ---- the next item: query group, KV head, part of the heads, tiles [t0, t1) ----
-    Slot x = find_slot(a, pl, cu, pos0, slot);
+    const Slot x = find_slot(a, pl, a.cu, a.pos0, slot);
     const int64_t n_tiles = x.nq ? x.ct + x.rt : 0;
     if (u >= slot_at + n_tiles * pl.subs) {
       slot_at += n_tiles * pl.subs;
@@ -296,86 +331,107 @@ cache_attn_kernel(const CacheAttnArgs a, const Plan pl, float* __restrict__ ws_o
     const int t0 = (int)(u - item0), t1 = (int)min(u1 - item0, n_tiles);
     const int kvh = sub / pl.parts, h0 = kvh * G + (sub % pl.parts) * R;
     const int heads = min(kvh * G + G - h0, G > R ? R : G);  // heads of a query in this item
+    const int vis = x.bad || !a.cmp.k ? 0 : (int)(((int64_t)x.p0 + 1) / a.r);  // of the first query
     if (x.bad && tid == 0) raise_status(a.status, CSA_ERR_DEVICE_BOUNDS);
 
-    // step t of this warp: 16 keys; its rows are resolved a step before the copies are issued
-    auto position = [&](int t) -> int {  // of key lane & 15; -1: not there
-      const int k = t * kTile + warp * kStep + (lane & 15);
-      if (x.bad || t >= t1) return -1;
-      if (t < x.ct) {
-        if (k >= x.vis) return -1;
-        if (!a.idx) return k;
-        const int v = __ldg(a.idx + (int64_t)x.row0 * a.k_pad + k);
-        if (v < 0) return -1;
-        const int64_t e = (int64_t)v - (a.cu_cmp ? __ldg(a.cu_cmp + x.b) : 0);
-        if (e >= 0 && e < ((int64_t)x.p0 + 1) / a.r) return (int)e;
-        raise_status(a.status, CSA_ERR_DEVICE_BOUNDS);
-        return -1;
+    // Cache rows (block * H_kv + head) * block + row of the keys of steps [t, t + kAhead)
+    // of this warp, a lane a key: the list and table reads of all steps are in flight together.
+    auto look_up = [&](int t) {
+      int pos[kAhead], blk[kAhead];
+      uint32_t* to = rows + ((t - t0) / kAhead % 2) * (kAhead * kStep) + lane;
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int tt = t + i;
+        const int k = tt * kTile + warp * kStep + lane;
+        pos[i] = -1;
+        if (!x.bad && tt < t1) {
+          if (tt < x.ct) {
+            if (k < x.vis) pos[i] = a.idx ? __ldg(a.idx + (int64_t)x.row0 * a.k_pad + k) : k;
+          } else {
+            const int p = x.w0 + k - x.ct * kTile;
+            if (p >= x.p0 - a.window + 1 && p < x.p0 + x.nq) pos[i] = p;
+          }
+        }
       }
-      const int p = x.w0 + k - x.ct * kTile;
-      return p >= x.p0 - a.window + 1 && p < x.p0 + x.nq ? p : -1;
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const bool entry = t + i < x.ct;
+        if (entry && a.idx && pos[i] >= 0) {
+          const int64_t e = (int64_t)pos[i] - (a.cu_cmp ? __ldg(a.cu_cmp + x.b) : 0);
+          pos[i] = e >= 0 && e < vis ? (int)e : -1;
+          if (pos[i] < 0) raise_status(a.status, CSA_ERR_DEVICE_BOUNDS);
+        }
+        const CacheView& cc = entry ? a.cmp : a.raw;
+        blk[i] = pos[i] >= 0 ? __ldg(cc.table + (int64_t)x.b * cc.max_blocks + (pos[i] >> cc.log_block)) : 0;
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const CacheView& cc = t + i < x.ct ? a.cmp : a.raw;
+        uint32_t row = kNoRow;
+        if (pos[i] >= 0) {
+          if (blk[i] >= 0 && blk[i] < cc.n_blocks)
+            row = ((uint32_t)(blk[i] * a.H_kv + kvh) << cc.log_block) + (pos[i] & ((1 << cc.log_block) - 1));
+          else
+            raise_status(a.status, CSA_ERR_DEVICE_BOUNDS);
+        }
+        to[i * kStep] = row;
+      }
     };
-    auto block_of = [&](int t, int pos) -> int {
-      return pos >= 0 ? cache_block(t < x.ct ? a.cmp : a.raw, x.b, pos, a.status) : -1;
-    };
-    auto copy = [&](int t, int pos, int blk) {
+    auto copy = [&](int t) {  // step t's codes and scales into its stage
       if (t < t1) {
+        const int n = t - t0;
+        const uint32_t* from = rows + (n % (2 * kAhead)) * kStep;
         const CacheView& cc = t < x.ct ? a.cmp : a.raw;
-        const uint32_t st = ring + (t % kStages) * L::kStage;
-        const int bh = blk >= 0 ? blk * a.H_kv + kvh : -1;
-        const int r = pos & ((1 << cc.log_block) - 1);
+        const uint32_t st = ring + (n % kStages) * L::kStage;
         constexpr int kPerRow = D / 16, kRowsPer = 32 / kPerRow;
+        const int r0 = lane / kPerRow, ch = lane % kPerRow;
+        const uint8_t* k = cc.k + ch * 16;
+        const uint8_t* v = kShared ? nullptr : cc.v + ch * 16;
 #pragma unroll
         for (int i = 0; i < kStep / kRowsPer; ++i) {
-          const int row = lane / kPerRow + i * kRowsPer, ch = lane % kPerRow;
-          const int rb = __shfl_sync(0xffffffffu, bh, row), rr = __shfl_sync(0xffffffffu, r, row);
-          const int64_t off = rb >= 0 ? ((((int64_t)rb << cc.log_block) + rr) * D + ch * 16) : 0;
-          cp_async_16_zfill(st + code_offset<D>(row, ch), cc.k + off, rb >= 0);
-          if (!kShared) cp_async_16_zfill(st + L::kCodes + code_offset<D>(row, ch), cc.v + off, rb >= 0);
+          const uint32_t row = from[r0 + i * kRowsPer];
+          const uint64_t off = row == kNoRow ? 0 : (uint64_t)row * D;
+          const uint32_t dst = st + code_offset<D>(r0 + i * kRowsPer, ch);
+          cp_async_16_zfill(dst, k + off, row != kNoRow);
+          if (!kShared) cp_async_16_zfill(dst + L::kCodes, v + off, row != kNoRow);
         }
-        const float* sc = lane < 16 || kShared ? cc.k_scale : cc.v_scale;
-        cp_async_4_zfill(st + L::kStage - 2 * kStep * 4 + lane * 4, sc + max(bh, 0), bh >= 0);
+        const uint32_t row = from[lane], bh = row == kNoRow ? 0 : row >> cc.log_block;
+        const uint32_t dst = st + L::kStage - 2 * kStep * 4 + lane * 4;
+        cp_async_4_zfill(dst, cc.k_scale + bh, row != kNoRow);
+        if (!kShared) cp_async_4_zfill(dst + kStep * 4, cc.v_scale + bh, row != kNoRow);
       }
       cp_async_commit();
     };
-    int pos_c, blk_c, pos_n;  // rows of the step to copy next, positions of the one after it
-    {
-      int pos[kStages], blk[kStages];
+    look_up(t0);
+    __syncwarp();
 #pragma unroll
-      for (int i = 0; i < kStages; ++i) pos[i] = position(t0 + i);
-#pragma unroll
-      for (int i = 0; i < kStages; ++i) blk[i] = block_of(t0 + i, pos[i]);
-#pragma unroll
-      for (int i = 0; i < kStages - 1; ++i) copy(t0 + i, pos[i], blk[i]);
-      pos_c = pos[kStages - 1];
-      blk_c = blk[kStages - 1];
-      pos_n = position(t0 + kStages);
-    }
+    for (int i = 0; i < kStages - 1; ++i) copy(t0 + i);
 
+    if (warp == kWarps - 1) {
+      for (int i = lane; i < R * D / 32; i += 32) s_nan[i] = 0;
+      if (lane == 0) s_nans = 0;
+    }
     // ---- queries as product fragments, one warp a 16-row tile ----
     if (warp < MT) {
-      float amax[2] = {0.f, 0.f};
-      const T* src[2];
+      float v[2][D / 4];  // this thread's 16-element chunks c (and c + 4) of rows g, g + 8
+      float inv[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int r = warp * 16 + g + 8 * e;
         const int qi = G > R ? 0 : r / G, h = G > R ? r : r % G;
         const bool real = qi < x.nq && h < heads;
-        const int at = real ? (x.row0 + qi) * a.H + h0 + h : -1;
         if (c == 0) {
           s_p[r] = real ? x.p0 + qi : -1;
-          s_out[r] = at;
+          s_vis[r] = real && a.cmp.k ? (int)(((int64_t)x.p0 + qi + 1) / a.r) : 0;
+          s_out[r] = real ? (x.row0 + qi) * a.H + h0 + h : -1;
         }
-        src[e] = at >= 0 ? static_cast<const T*>(a.q) + (int64_t)(x.row0 + qi) * a.H * D + (int64_t)(h0 + h) * D : nullptr;
-      }
-      float v[2][D / 4];  // this thread's 16-element chunks c (and c + 4)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
+        const T* src = static_cast<const T*>(a.q) + ((int64_t)(x.row0 + qi) * a.H + h0 + h) * D;
+        float amax = 0.f;
 #pragma unroll
         for (int i = 0; i < D / 4; i += 4) {
           float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (src[e]) {
-            const T* p = src[e] + 16 * (c + 4 * (i / 16)) + i % 16;
+          if (real) {
+            const T* p = src + 16 * (c + 4 * (i / 16)) + i % 16;
             if (kSplit) {
               f = __ldg(reinterpret_cast<const float4*>(p));
             } else {
@@ -387,249 +443,307 @@ cache_attn_kernel(const CacheAttnArgs a, const Plan pl, float* __restrict__ ws_o
         }
 #pragma unroll
         for (int i = 0; i < D / 4; ++i)
-          if (fabsf(v[e][i]) < INFINITY) amax[e] = fmaxf(amax[e], fabsf(v[e][i]));
-        amax[e] = fmaxf(amax[e], __shfl_xor_sync(0xffffffffu, amax[e], 1));
-        amax[e] = fmaxf(amax[e], __shfl_xor_sync(0xffffffffu, amax[e], 2));
-      }
-      float inv[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
+          if (fabsf(v[e][i]) < INFINITY) amax = fmaxf(amax, fabsf(v[e][i]));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
         // largest element to [2^14, 2^15), as far as 2^e and 2^-e are normal numbers
-        const int ex = max((int)(__float_as_uint(amax[e]) >> 23) - 127 - 14, -113);
-        inv[e] = pow2i(-ex);
-        if (c == 0) s_qf[warp * 16 + g + 8 * e] = pow2i(ex);
+        const int ex = max((int)(__float_as_uint(amax) >> 23) - 127 - 14, -113);
+        inv[e] = a.scale < 0.f ? -pow2i(-ex) : pow2i(-ex);
+        if (c == 0) s_qf[r] = pow2i(ex);
       }
 #pragma unroll
       for (int ks = 0; ks < D / 16; ++ks) {
-        uint4 hi, lo;
-        uint32_t* hw = reinterpret_cast<uint32_t*>(&hi);
-        uint32_t* lw = reinterpret_cast<uint32_t*>(&lo);
+        uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {  // a0: row g, first pair; a1: row g + 8; a2, a3: second pair
+        for (int w = 0; w < 4; ++w) {  // row g, first pair; row g + 8; their second pairs
           const int e = w & 1, i = ks * 4 + (w >> 1) * 2;
           const float f0 = v[e][i] * inv[e], f1 = v[e][i + 1] * inv[e];
-          hw[w] = pack_f16x2(f0, f1);
-          lw[w] = rest_f16x2(hw[w], f0, f1);
+          hi[w] = pack_f16x2(f0, f1);
+          lo[w] = rest_f16x2(hi[w], f0, f1);
         }
         const uint32_t at = qbuf + ((warp * (D / 16) + ks) * 32 + lane) * 16;
-        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(hi.x), "r"(hi.y), "r"(hi.z), "r"(hi.w));
+        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(hi[0]), "r"(hi[1]), "r"(hi[2]), "r"(hi[3]));
         if (kSplit)
-          asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at + L::kQ / 2), "r"(lo.x), "r"(lo.y), "r"(lo.z),
-                       "r"(lo.w));
+          asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at + L::kQ / 2), "r"(lo[0]), "r"(lo[1]),
+                       "r"(lo[2]), "r"(lo[3]));
       }
     }
     __syncthreads();
-    uint4 qr[L::kQRegs ? D / 16 : 1];
-    if (L::kQRegs) {
-#pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks) qr[ks] = lds128(qbuf + (ks * 32 + lane) * 16);
-    }
-    float qf[MT][2], m[MT][2], M[MT][2], l[MT][2], o[MT][D / 8][4];
+    float qf[MT][2], M[MT][2], l[MT][2], o[MT][D / 8][4];
+    float e0 = 0.f;         // l is of 2^(t + e0 - M + kBase), e0 the first key's V exponent
+    bool any_key = false, any_far = false;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         qf[mt][e] = s_qf[mt * 16 + g + 8 * e];
-        m[mt][e] = M[mt][e] = -INFINITY;
+        M[mt][e] = kNone;
         l[mt][e] = 0.f;
       }
 #pragma unroll
       for (int i = 0; i < D / 8; ++i) o[mt][i][0] = o[mt][i][1] = o[mt][i][2] = o[mt][i][3] = 0.f;
     }
-    const float scale_log2 = a.scale * kLog2e;
 
     for (int t = t0; t < t1; ++t) {
       cp_async_wait<kStages - 2>();
       __syncwarp();
-      copy(t + kStages - 1, pos_c, blk_c);
-      pos_c = pos_n;
-      blk_c = block_of(t + kStages, pos_n);
-      pos_n = position(t + kStages + 1);
-      const uint32_t st = ring + (t % kStages) * L::kStage;
-      const uint32_t sc = st + L::kStage - 2 * kStep * 4;
-      float ks[4], ev[4];  // keys 2c, 2c + 1, 8 + 2c, 9 + 2c
-      {
-        const float2 k0 = lds_f2(sc + 8 * c), k1 = lds_f2(sc + 32 + 8 * c);
-        const float2 v0 = lds_f2(sc + 64 + 8 * c), v1 = lds_f2(sc + 96 + 8 * c);
-        ks[0] = k0.x, ks[1] = k0.y, ks[2] = k1.x, ks[3] = k1.y;
-        ev[0] = v0.x, ev[1] = v0.y, ev[2] = v1.x, ev[3] = v1.y;
+      if ((t - t0) % kAhead == 0 && t + kAhead < t1) {
+        look_up(t + kAhead);
+        __syncwarp();
       }
-      if (!__any_sync(0xffffffffu, fmaxf(fmaxf(ks[0], ks[1]), fmaxf(ks[2], ks[3])) > 0.f)) continue;  // no key here
-#pragma unroll
-      for (int i = 0; i < 4; ++i) ev[i] = (float)((int)(__float_as_uint(ev[i]) >> 23) - 127);
+      copy(t + kStages - 1);
+      const uint32_t st = ring + ((t - t0) % kStages) * L::kStage;
+      const uint32_t sc = st + L::kStage - 2 * kStep * 4;
+      // each key's score factor and V exponent, in place of its scales
+      bool uniform, far;    // one V scale in each half of the step (a block's); a V scale far from e0
+      float ie[2];
+      {
+        const float ks = lds_f(sc + 4 * lane), vs = kShared ? ks : lds_f(sc + kStep * 4 + 4 * lane);
+        const uint32_t there = __ballot_sync(0xffffffffu, ks > 0.f);
+        if (there == 0) continue;
+        const float ev = exponent_of(vs);
+        if (!any_key) e0 = __shfl_sync(0xffffffffu, ev, __ffs(there) - 1);
+        any_key = true;
+        far = __any_sync(0xffffffffu, ks > 0.f && fabsf(ev - e0) > 60.f);
+        const float ev0 = __shfl_sync(0xffffffffu, ev, 0), ev1 = __shfl_sync(0xffffffffu, ev, 16);
+        ie[0] = ex2(e0 - ev0);
+        ie[1] = ex2(e0 - ev1);
+        uniform = __all_sync(0xffffffffu, ks > 0.f && ev == (lane < 16 ? ev0 : ev1));
+        asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(sc + 8 * lane), "f"(ks * scale_log2),
+                     "f"(ks > 0.f ? ev : -INFINITY)
+                     : "memory");
+        __syncwarp();
+      }
+
       // ---- S = Q K^T ----
-      float s[MT][2][4];
+      float s[MT][4][4];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) s[mt][j][0] = s[mt][j][1] = s[mt][j][2] = s[mt][j][3] = 0.f;
+        for (int j = 0; j < 4; ++j) s[mt][j][0] = s[mt][j][1] = s[mt][j][2] = s[mt][j][3] = 0.f;
 #pragma unroll
       for (int h = 0; h < D / 64; ++h) {
-        const uint4 k0 = lds128(st + off_k[h]), k1 = lds128(st + off_k[h] + 8 * D);
-        const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
+        uint32_t kw[4][4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint4 k = lds128(st + off_k[h] + j * 8 * D);
+          kw[j][0] = k.x, kw[j][1] = k.y, kw[j][2] = k.z, kw[j][3] = k.w;
+        }
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-          const uint32_t b00 = widen_lo(w0[w]), b01 = widen_hi(w0[w]), b10 = widen_lo(w1[w]), b11 = widen_hi(w1[w]);
+          uint4 q[MT], ql[MT];
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
             const uint32_t at = qbuf + ((mt * (D / 16) + h * 4 + w) * 32 + lane) * 16;
-            const uint4 q = L::kQRegs ? qr[L::kQRegs ? h * 4 + w : 0] : lds128(at);
-            mma_f16(s[mt][0], q, b00, b01);
-            mma_f16(s[mt][1], q, b10, b11);
-            if (kSplit) {
-              const uint4 ql = lds128(at + L::kQ / 2);
-              mma_f16(s[mt][0], ql, b00, b01);
-              mma_f16(s[mt][1], ql, b10, b11);
+            q[mt] = lds128(at);
+            if (kSplit) ql[mt] = lds128(at + L::kQ / 2);
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t b0 = widen_lo(kw[j][w]), b1 = widen_hi(kw[j][w]);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              mma_f16(s[mt][j], q[mt], b0, b1);
+              if (kSplit) mma_f16(s[mt][j], ql[mt], b0, b1);
             }
           }
         }
       }
-      // ---- log2 scores, masks ----
-      bool seen[4];
+
+      // a step that some of the item's queries see and others do not
+      const bool entries = t < x.ct;
+      const int first = t * kTile + warp * kStep + (entries ? 0 : x.w0 - x.ct * kTile);
+      bool mixed = false;
+      if (x.nq > 1)
+        mixed = entries ? first + kStep > vis : first + kStep - 1 > x.p0 || first <= x.p0 + x.nq - 1 - a.window;
+
+      // ---- softmax: s becomes u = t + e, then the weights 2^(u - M + kBase) ----
+      float ev[8];  // keys 8 j + 2 c, + 1
+      {
+        float ks[8];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        seen[i] = ks[i] > 0.f;
-        ks[i] *= scale_log2;
+        for (int j = 0; j < 4; ++j) {
+          const uint4 k = lds128(sc + 64 * j + 16 * c);
+          ks[2 * j] = __uint_as_float(k.x), ev[2 * j] = __uint_as_float(k.y);
+          ks[2 * j + 1] = __uint_as_float(k.z), ev[2 * j + 1] = __uint_as_float(k.w);
+        }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              s[mt][j][i] = fmaf(s[mt][j][i] * ks[2 * j + (i & 1)], qf[mt][i >> 1], ev[2 * j + (i & 1)]);
+      }
+      if (mixed) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int r = mt * 16 + g + 8 * e, p = s_p[r];
+            const int from = (entries ? 0 : p - a.window + 1) - first, to = (entries ? s_vis[r] : p + 1) - first;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int at = (i >> 1) * 8 + 2 * c + (i & 1);
+              if (at < from || at >= to) s[mt][i >> 1][2 * e + (i & 1)] = -INFINITY;
+            }
+          }
+      }
+      {
+        float top[MT][2];
+        bool grow = false;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float v = fmaxf(s[mt][0][2 * e], s[mt][0][2 * e + 1]);
+#pragma unroll
+            for (int j = 1; j < 4; ++j) v = fmaxf(v, fmaxf(s[mt][j][2 * e], s[mt][j][2 * e + 1]));
+            top[mt][e] = v;
+            grow |= v > M[mt][e] + kSlack;
+          }
+        if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            float f[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float v = fmaxf(top[mt][e], __shfl_xor_sync(0xffffffffu, top[mt][e], 1));
+              v = fmaxf(M[mt][e], fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2)));
+              f[e] = ex2(M[mt][e] - v);
+              l[mt][e] *= f[e];
+              M[mt][e] = v;
+            }
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+              o[mt][i][0] *= f[0];
+              o[mt][i][1] *= f[0];
+              o[mt][i][2] *= f[1];
+              o[mt][i][3] *= f[1];
+            }
+          }
+        }
+      }
+      if (far) {  // block scales 2^60 apart: this step's part of the sums in sums of their own
+        if (!any_far) {
+          for (int i = lane; i < R; i += 32) far_m[i] = kNone, far_l[i] = 0.f;
+          __syncwarp();
+        }
+        any_far = true;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int r = mt * 16 + g + 8 * e;
+            float top = kNone, sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (ev[i] > -INFINITY) top = fmaxf(top, s[mt][i >> 1][2 * e + (i & 1)] - ev[i]);
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(far_m[r], fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2)));
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (ev[i] > -INFINITY) sum += ex2(s[mt][i >> 1][2 * e + (i & 1)] - ev[i] - top);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+            if (c == 0) {
+              far_l[r] = far_l[r] * ex2(far_m[r] - top) + sum;
+              far_m[r] = top;
+            }
+          }
+        __syncwarp();
       }
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int key = 2 * j + (e & 1);
-            s[mt][j][e] = seen[key] ? s[mt][j][e] * ks[key] * qf[mt][e >> 1] : -INFINITY;
-          }
-      // a step that some of the item's queries see and others do not
-      const bool entries = t < x.ct;
-      const int first = entries ? t * kTile + warp * kStep : x.w0 + (t - x.ct) * kTile + warp * kStep;
-      auto sees = [&](int p, int pos) {  // entry / row pos, query at p
-        return entries ? pos < ((int64_t)p + 1) / a.r : pos <= p && pos > p - a.window;
-      };
-      bool mixed = false;
-      if (x.nq > 1) {
-        const int p1 = x.p0 + x.nq - 1;
-        mixed = !sees(x.p0, first + kStep - 1) || !(entries || first > p1 - a.window);
-        if (mixed) {
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int p = s_p[mt * 16 + g + 8 * e];
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (!sees(p, first + (i >> 1) * 8 + 2 * c + (i & 1))) s[mt][i >> 1][2 * e + (i & 1)] = -INFINITY;
-            }
-        }
-      }
-      // ---- softmax: l against m, the products' weights against M ----
-      uint4 pa[MT], pl_[MT];
-      bool grew = false;
-      float beta[MT][2];
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        float w[2][4];
-#pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float t4[4], u4[4];
+          const float shift = kBase - M[mt][e];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            t4[i] = s[mt][i >> 1][2 * e + (i & 1)];
-            u4[i] = t4[i] + ev[i];
+          for (int i = 0; i < 8; ++i) {
+            float& w = s[mt][i >> 1][2 * e + (i & 1)];
+            w = ex2(w + shift);
           }
-          float tm = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
-          float um = fmaxf(fmaxf(u4[0], u4[1]), fmaxf(u4[2], u4[3]));
-          tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 1));
-          um = fmaxf(um, __shfl_xor_sync(0xffffffffu, um, 1));
-          tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 2));
-          um = fmaxf(um, __shfl_xor_sync(0xffffffffu, um, 2));
-          const float mn = fmaxf(m[mt][e], tm), Mn = fmaxf(M[mt][e], um);
-          const float mu = mn == -INFINITY ? 0.f : mn, Mu = Mn == -INFINITY ? 0.f : Mn;
-          float sum = 0.f;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            sum += ex2(t4[i] - mu);
-            w[e][i] = ex2(u4[i] - Mu + 15.f);
-          }
-          l[mt][e] = l[mt][e] * ex2(m[mt][e] - mu) + sum;
-          beta[mt][e] = ex2(M[mt][e] - Mu);
-          grew |= Mn > M[mt][e];
-          m[mt][e] = mn;
-          M[mt][e] = Mn;
         }
-        pa[mt] = make_uint4(pack_f16x2(w[0][0], w[0][1]), pack_f16x2(w[1][0], w[1][1]), pack_f16x2(w[0][2], w[0][3]),
-                            pack_f16x2(w[1][2], w[1][3]));
-        if (kSplit)
-          pl_[mt] = make_uint4(rest_f16x2(pa[mt].x, w[0][0], w[0][1]), rest_f16x2(pa[mt].y, w[1][0], w[1][1]),
-                               rest_f16x2(pa[mt].z, w[0][2], w[0][3]), rest_f16x2(pa[mt].w, w[1][2], w[1][3]));
-      }
-      if (__any_sync(0xffffffffu, grew)) {
+      if (far) {
+      } else if (uniform) {
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
-            o[mt][i][0] *= beta[mt][0];
-            o[mt][i][1] *= beta[mt][0];
-            o[mt][i][2] *= beta[mt][1];
-            o[mt][i][3] *= beta[mt][1];
-          }
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf)
+              l[mt][e] = fmaf((s[mt][2 * hf][2 * e] + s[mt][2 * hf][2 * e + 1]) +
+                                  (s[mt][2 * hf + 1][2 * e] + s[mt][2 * hf + 1][2 * e + 1]),
+                              ie[hf], l[mt][e]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float f = ev[i] > -INFINITY ? ex2(e0 - ev[i]) : 0.f;
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) l[mt][e] = fmaf(s[mt][i >> 1][2 * e + (i & 1)], f, l[mt][e]);
+        }
       }
-      // ---- O += P V: keys 2c, 2c + 1, 8 + 2c, 9 + 2c; column n of product i is dim n D / 8 + i ----
+      uint4 pa[MT][2], pb[MT][2];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          const float(&w0)[4] = s[mt][2 * hf];
+          const float(&w1)[4] = s[mt][2 * hf + 1];
+          uint4& p = pa[mt][hf];
+          p = make_uint4(pack_f16x2(w0[0], w0[1]), pack_f16x2(w0[2], w0[3]), pack_f16x2(w1[0], w1[1]),
+                         pack_f16x2(w1[2], w1[3]));
+          if (kSplit)
+            pb[mt][hf] = make_uint4(rest_f16x2(p.x, w0[0], w0[1]), rest_f16x2(p.y, w0[2], w0[3]),
+                                    rest_f16x2(p.z, w1[0], w1[1]), rest_f16x2(p.w, w1[2], w1[3]));
+        }
+
+      // ---- O += P V, 16 keys at a time: 2c, 2c + 1, 8 + 2c, 9 + 2c of them a thread;
+      //      column n of product i is dim n D / 8 + i ----
       constexpr int kWords = D / 32;
-      uint32_t v[4][kWords];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const uint32_t at = st + (kShared ? 0 : L::kCodes) + off_v[k & 1] + (k >> 1) * 8 * D;
-        if (D == 128) {
-          const uint4 q = lds128(at);
-          v[k][0] = q.x, v[k][1] = q.y, v[k][kWords - 2] = q.z, v[k][kWords - 1] = q.w;
-        } else {
-          const uint2 q = lds64(at);
-          v[k][0] = q.x, v[k][1] = q.y;
+      for (int hf = 0; hf < 2; ++hf) {
+        uint32_t v[4][kWords];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t at = st + (kShared ? 0 : L::kCodes) + off_v[k & 1] + (2 * hf + (k >> 1)) * 8 * D;
+          if (D == 128) {
+            const uint4 q = lds128(at);
+            v[k][0] = q.x, v[k][1] = q.y, v[k][kWords - 2] = q.z, v[k][kWords - 1] = q.w;
+          } else {
+            const uint2 q = lds64(at);
+            v[k][0] = q.x, v[k][1] = q.y;
+          }
         }
-      }
-      bool nan = false;  // a NaN row that only some queries see must not reach the others as 0 * NaN
-      if (mixed) {
+        if (mixed) {  // a NaN that only some queries see must not reach the others as 0 * NaN: noted, and taken as 0
+          bool nan = false;
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+          for (int k = 0; k < 4; ++k)
 #pragma unroll
-          for (int w = 0; w < kWords; ++w) nan |= has_nan4(v[k][w]);
-        nan = __any_sync(0xffffffffu, nan);
-      }
+            for (int w = 0; w < kWords; ++w) nan |= has_nan4(v[k][w]);
+          if (__any_sync(0xffffffffu, nan)) {
+            note_nans<D, R>(st + (kShared ? 0 : L::kCodes), hf, first, entries, a.window, s_p, s_vis, s_nan, lane);
+            if (lane == 0) s_nans = 1;
 #pragma unroll
-      for (int w = 0; w < kWords; ++w) {
-        uint32_t y0[2], y1[2];
+            for (int k = 0; k < 4; ++k)
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          y0[hh] = __byte_perm(v[0][w], v[1][w], hh ? 0x7362 : 0x5140);
-          y1[hh] = __byte_perm(v[2][w], v[3][w], hh ? 0x7362 : 0x5140);
+              for (int w = 0; w < kWords; ++w) v[k][w] = without_nan4(v[k][w]);
+          }
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t b0 = (i & 1) ? widen_hi(y0[i >> 1]) : widen_lo(y0[i >> 1]);
-          const uint32_t b1 = (i & 1) ? widen_hi(y1[i >> 1]) : widen_lo(y1[i >> 1]);
-          if (!nan) {
+        for (int w = 0; w < kWords; ++w) {
+          const uint32_t y[2][2] = {{__byte_perm(v[0][w], v[1][w], 0x5140), __byte_perm(v[0][w], v[1][w], 0x7362)},
+                                    {__byte_perm(v[2][w], v[3][w], 0x5140), __byte_perm(v[2][w], v[3][w], 0x7362)}};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t b0 = (i & 1) ? widen_hi(y[0][i >> 1]) : widen_lo(y[0][i >> 1]);
+            const uint32_t b1 = (i & 1) ? widen_hi(y[1][i >> 1]) : widen_lo(y[1][i >> 1]);
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
-              mma_f16(o[mt][4 * w + i], pa[mt], b0, b1);
-              if (kSplit) mma_f16(o[mt][4 * w + i], pl_[mt], b0, b1);
-            }
-          } else {  // query by query, without the rows that it does not see
-            for (int qi = 0; qi < x.nq; ++qi) {
-              uint32_t z0 = b0, z1 = b1;
-              const int k0 = first + 2 * c, p = x.p0 + qi;
-              if (!sees(p, k0)) z0 &= 0xffff0000u;
-              if (!sees(p, k0 + 1)) z0 &= 0x0000ffffu;
-              if (!sees(p, k0 + 8)) z1 &= 0xffff0000u;
-              if (!sees(p, k0 + 9)) z1 &= 0x0000ffffu;
-#pragma unroll
-              for (int mt = 0; mt < MT; ++mt) {
-                float d[4] = {0.f, 0.f, 0.f, 0.f};
-                mma_f16(d, pa[mt], z0, z1);
-                if (kSplit) mma_f16(d, pl_[mt], z0, z1);
-                if (s_p[mt * 16 + g] == p) o[mt][4 * w + i][0] += d[0], o[mt][4 * w + i][1] += d[1];
-                if (s_p[mt * 16 + g + 8] == p) o[mt][4 * w + i][2] += d[2], o[mt][4 * w + i][3] += d[3];
-              }
+              mma_f16(o[mt][4 * w + i], pa[mt][hf], b0, b1);
+              if (kSplit) mma_f16(o[mt][4 * w + i], pb[mt][hf], b0, b1);
             }
           }
         }
@@ -638,6 +752,11 @@ cache_attn_kernel(const CacheAttnArgs a, const Plan pl, float* __restrict__ ws_o
     cp_async_wait<0>();
 
     // ---- join the four warps ----
+    __syncthreads();  // the rings are free
+    float* acc = reinterpret_cast<float*>(smem);
+    float(*s_m)[R] = reinterpret_cast<float(*)[R]>(smem + L::kMerge);
+    float(*s_M)[R] = s_m + kWarps;
+    float(*s_l)[R] = s_M + kWarps;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -646,14 +765,19 @@ cache_attn_kernel(const CacheAttnArgs a, const Plan pl, float* __restrict__ ws_o
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
         const int r = mt * 16 + g + 8 * e;
+        float m = M[mt][e] == kNone ? kNone : M[mt][e] - kBase - e0;  // the sum is sum * 2^m
+        if (any_far) {
+          const float top = fmaxf(m, far_m[r]);
+          sum = sum * ex2(m - top) + far_l[r] * ex2(far_m[r] - top);
+          m = top;
+        }
         if (c == 0) {
-          s_m[warp][r] = m[mt][e];
+          s_m[warp][r] = m;
           s_M[warp][r] = M[mt][e];
           s_l[warp][r] = sum;
         }
       }
-    __syncthreads();  // the rings are free, too
-    float* acc = reinterpret_cast<float*>(smem);
+    __syncthreads();
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -662,7 +786,7 @@ cache_attn_kernel(const CacheAttnArgs a, const Plan pl, float* __restrict__ ws_o
         float top = s_M[0][r];
 #pragma unroll
         for (int w = 1; w < kWarps; ++w) top = fmaxf(top, s_M[w][r]);
-        const float f = M[mt][e] == -INFINITY ? 0.f : ex2(M[mt][e] - top);
+        const float f = ex2(M[mt][e] - top);
         // columns 2c and 2c + 1 of products 0 .. D / 8 - 1: dims [2c D/8, (2c + 2) D/8)
 #pragma unroll
         for (int h = 0; h < 2; ++h)
@@ -670,7 +794,6 @@ cache_attn_kernel(const CacheAttnArgs a, const Plan pl, float* __restrict__ ws_o
           for (int i = 0; i < D / 8; i += 4) {
             float4 v = make_float4(o[mt][i][2 * e + h], o[mt][i + 1][2 * e + h], o[mt][i + 2][2 * e + h],
                                    o[mt][i + 3][2 * e + h]);
-            if (f == 0.f) v = make_float4(0.f, 0.f, 0.f, 0.f);
             v.x *= f, v.y *= f, v.z *= f, v.w *= f;
             *reinterpret_cast<float4*>(acc + (warp * R + r) * D + (2 * c + h) * (D / 8) + i) = v;
           }
@@ -683,7 +806,7 @@ cache_attn_kernel(const CacheAttnArgs a, const Plan pl, float* __restrict__ ws_o
       const int at = s_out[r];
       if (at < 0) continue;
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      float mm = -INFINITY, MM = -INFINITY, ll = 0.f;
+      float mm = kNone, MM = kNone, ll = 0.f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         const float4 f = *reinterpret_cast<const float4*>(acc + (w * R + r) * D + 4 * d4);
@@ -692,7 +815,14 @@ cache_attn_kernel(const CacheAttnArgs a, const Plan pl, float* __restrict__ ws_o
         MM = fmaxf(MM, s_M[w][r]);
       }
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) ll += s_m[w][r] == -INFINITY ? s_l[w][r] : s_l[w][r] * ex2(s_m[w][r] - mm);
+      for (int w = 0; w < kWarps; ++w) ll += s_l[w][r] * ex2(s_m[w][r] - mm);
+      if (s_nans) {
+        const uint32_t bits = s_nan[(r * D + 4 * d4) / 32] >> (4 * d4 % 32);
+        if (bits & 1) v.x = NAN;
+        if (bits & 2) v.y = NAN;
+        if (bits & 4) v.z = NAN;
+        if (bits & 8) v.w = NAN;
+      }
       if (!whole) {
         *reinterpret_cast<float4*>(piece + r * D + 4 * d4) = v;
         if (d4 == 0) {
@@ -733,7 +863,7 @@ cache_attn_join_kernel(const CacheAttnArgs a, const Plan pl, const float* __rest
   const int qi = G > R ? 0 : r / G, h = G > R ? r : r % G;
   if (qi >= meta.y || h >= heads) return;
   auto piece = [&](int cta) { return ws_o + ((int64_t)cta * 2 + (cta == first ? 1 : 0)) * piece_floats<D>(R); };
-  float m = -INFINITY, M = -INFINITY;
+  float m = kNone, M = kNone;
   for (int k = first + lane; k <= last; k += 32) {
     m = fmaxf(m, piece(k)[R * D + r]);
     M = fmaxf(M, piece(k)[R * D + R + r]);
@@ -751,11 +881,9 @@ cache_attn_join_kernel(const CacheAttnArgs a, const Plan pl, const float* __rest
     const float* p = piece(k);
     const float4 x = *reinterpret_cast<const float4*>(p + r * D + 4 * d4);
     const float pm = p[R * D + r], pM = p[R * D + R + r], q = p[R * D + 2 * R + r];
-    l += pm == -INFINITY ? q : q * ex2(pm - m);
-    if (pM > -INFINITY) {
-      const float f = ex2(pM - M);
-      v.x += x.x * f, v.y += x.y * f, v.z += x.z * f, v.w += x.w * f;
-    }
+    l += q * ex2(pm - m);
+    const float f = ex2(pM - M);
+    v.x += x.x * f, v.y += x.y * f, v.z += x.z * f, v.w += x.w * f;
   }
   if (lane < D / 4) finish_row<T, D>(a, (meta.x + qi) * a.H + h0 + h, d4, v, m, M, l);
 }
@@ -769,7 +897,7 @@ constexpr int ctas_per_sm(int mt) { return mt == 1 ? 3 : 2; }
 
 size_t ws_bytes(int sm_count, int mt, int d) {
   const size_t grid = (size_t)sm_count * ctas_per_sm(mt);
-  return grid * (sizeof(int4) + 2 * sizeof(float) * (size_t)(16 * mt) * (d + 4));
+  return grid * (sizeof(int4) + sizeof(float) * (size_t)(16 * mt) * (2 * (d + 4) + 2 * kWarps));
 }
 
 template <typename T, int D, int MT, bool kShared>
@@ -784,10 +912,11 @@ cudaError_t run(const CacheAttnArgs& a, int sm_count, cudaStream_t stream) {
   const int grid = sm_count * ctas_per_sm(MT);
   int4* meta = static_cast<int4*>(a.ws);
   float* pieces = reinterpret_cast<float*>(meta + grid);
+  float* far = pieces + (size_t)grid * 2 * piece_floats<D>(L::R);
   cudaError_t e = cudaFuncSetAttribute(cache_attn_kernel<T, D, MT, kShared>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
   if (e != cudaSuccess) return e;
-  cache_attn_kernel<T, D, MT, kShared><<<grid, kThreads, L::kSmem, stream>>>(a, pl, pieces, meta);
+  cache_attn_kernel<T, D, MT, kShared><<<grid, kThreads, L::kSmem, stream>>>(a, pl, pieces, meta, far);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid, L::R / kWarps);

@@ -449,7 +449,8 @@ typedef struct csa_cache_s {
   float* k_scale;        /* [n_blocks, H_kv] */
   float* v_scale;        /* the same, set exactly when v is */
   const int32_t* table;  /* [B, max_blocks] block numbers, 0 .. n_blocks - 1 */
-  int n_blocks, max_blocks;  /* max_blocks * block at most 2^30, n_blocks * H_kv below 2^31 */
+  int n_blocks, max_blocks;  /* max_blocks * block at most 2^30; n_blocks * H_kv
+                               below 2^31 and times block below 2^32 - 1 */
   int block;             /* rows of a block: 16, 32, 64 or 128 */
   int H_kv, d;           /* d 64 or 128 */
 } csa_cache_t;
