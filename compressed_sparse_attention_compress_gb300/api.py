@@ -330,17 +330,17 @@ class _CacheStruct(ctypes.Structure):
                 ("max_blocks", ctypes.c_int), ("block", ctypes.c_int), ("H_kv", ctypes.c_int), ("d", ctypes.c_int)]
 
 
-def _want(what, t, dtype, shape, device=None):
-    """t is a contiguous tensor of this type and shape (None: any extent) on this device."""
+def _want(what, t, dtype, shape, device):
+    """Address of t: a contiguous tensor of this type and shape on this device (one short test when it is)."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype != dtype:
         raise TypeError(f"{what}: {t.dtype}, expected {dtype}")
-    if len(t.shape) != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape)):
-        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)} (None: any)")
-    if not t.is_contiguous():
-        raise ValueError(f"{what}: tensors passed to libcsa must be contiguous")
-    if device is not None and t.get_device() != device:
+    if t.shape != shape:
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.get_device() != device:
         raise ValueError(f"{what}: on {t.device}, expected cuda:{device}")
-    return t.data_ptr()
+    raise ValueError(f"{what}: tensors passed to libcsa must be contiguous")
 
 
 class Cache:
@@ -361,7 +361,9 @@ class Cache:
         s = _CacheStruct()
         s.k = _want("k", k, torch.uint8, (n, H_kv, block, d), dev)
         s.k_scale = _want("k_scale", k_scale, torch.float32, (n, H_kv), dev)
-        s.table = _want("table", table, torch.int32, (None, None), dev)
+        if table.dim() != 2:
+            raise ValueError(f"table: shape {tuple(table.shape)}, expected [B, max_blocks]")
+        s.table = _want("table", table, torch.int32, table.shape, dev)
         if v is not None:
             s.v = _want("v", v, torch.uint8, (n, H_kv, block, d), dev)
             s.v_scale = _want("v_scale", v_scale, torch.float32, (n, H_kv), dev)
@@ -373,23 +375,26 @@ class Cache:
 
 
 def _stream_of(h, stream):
-    return (stream if stream is not None else torch.cuda.current_stream(h.device)).cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(h.device)
 
 
-def _packing(h, cache, cu_seqlens, pos0):
+def _packing(h, caches, cu_seqlens, pos0):
     """Checked sequences of a cache call: (B, cu pointer, pos0 pointer)."""
-    B = cu_seqlens.numel() - 1
-    if cache.device != h.device:
-        raise ValueError(f"cache on cuda:{cache.device}, handle on cuda:{h.device}")
-    if B < 0 or cache.B < B:
-        raise ValueError(f"table has {cache.B} rows for {B} sequences")
+    B = cu_seqlens.shape[0] - 1
+    for c in caches:
+        if c.device != h.device:
+            raise ValueError(f"cache on cuda:{c.device}, handle on cuda:{h.device}")
+        if not 0 <= B <= c.B:
+            raise ValueError(f"table has {c.B} rows for {B} sequences")
     return (B, _want("cu_seqlens", cu_seqlens, torch.int32, (B + 1,), h.device),
             _want("pos0", pos0, torch.int32, (B,), h.device))
 
 
 def csa_cache_write(h: Handle, cache: Cache, x_k, cu_seqlens, pos0, x_v=None, stream=None):
     """Quantise rows [T_cap, H_kv, d] into the cache at positions pos0[b] + i."""
-    B, cu, p0 = _packing(h, cache, cu_seqlens, pos0)
+    B, cu, p0 = _packing(h, (cache,), cu_seqlens, pos0)
     shape = (x_k.shape[0], cache.H_kv, cache.d)
     k = _want("x_k", x_k, x_k.dtype, shape, h.device)
     v = _want("x_v", x_v, x_k.dtype, shape, h.device) if x_v is not None else None
@@ -399,7 +404,7 @@ def csa_cache_write(h: Handle, cache: Cache, x_k, cu_seqlens, pos0, x_v=None, st
 
 def csa_cache_read(h: Handle, cache: Cache, cu_seqlens, pos0, k_out, v_out=None, stream=None):
     """Rows at positions pos0[b] + i of the cache, dequantised into [T_cap, H_kv, d]."""
-    B, cu, p0 = _packing(h, cache, cu_seqlens, pos0)
+    B, cu, p0 = _packing(h, (cache,), cu_seqlens, pos0)
     shape = (k_out.shape[0], cache.H_kv, cache.d)
     k = _want("k_out", k_out, k_out.dtype, shape, h.device)
     v = _want("v_out", v_out, k_out.dtype, shape, h.device) if v_out is not None else None
@@ -415,20 +420,27 @@ def csa_cache_attn_fwd(h: Handle, q, cu_seqlens, pos0, softmax_scale: float, out
                        cu_cmp=None, ratio: int = 0, window: int = 0, sink=None, lse=None, stream=None):
     """Attention of q [T_cap, H, d] over a cache of compressed entries (all visible ones, or
     idx's) and the last ``window`` rows of a raw cache, in one softmax."""
-    if cmp is None and raw is None:
+    caches = [c for c in (cmp, raw) if c is not None]
+    if not caches:
         raise ValueError("neither cmp nor raw is given")
-    for c in (cmp, raw):
-        if c is not None:
-            B, cu, p0 = _packing(h, c, cu_seqlens, pos0)
-    T, H, d = q.shape
+    B, cu, p0 = _packing(h, caches, cu_seqlens, pos0)
     dev = h.device
-    ptr = [_want("q", q, q.dtype, (T, H, d), dev), _want("out", out, q.dtype, (T, H, d), dev)]
-    i = _want("idx", idx, torch.int32, (T, None), dev) if idx is not None else None
-    cc = _want("cu_cmp", cu_cmp, torch.int32, (B + 1,), dev) if cu_cmp is not None else None
-    sk = _want("sink", sink, torch.float32, (H,), dev) if sink is not None else None
-    ls = _want("lse", lse, torch.float32, (T, H), dev) if lse is not None else None
-    w = _want("ws", ws, ws.dtype, (None,), dev) if ws is not None else None
+    shape = q.shape
+    T, H, d = shape
+    k_pad, i, cc, sk, ls, w, n = 0, None, None, None, None, None, 0
+    if idx is not None:
+        k_pad = idx.shape[-1]
+        i = _want("idx", idx, torch.int32, (T, k_pad), dev)
+    if cu_cmp is not None:
+        cc = _want("cu_cmp", cu_cmp, torch.int32, (B + 1,), dev)
+    if sink is not None:
+        sk = _want("sink", sink, torch.float32, (H,), dev)
+    if lse is not None:
+        ls = _want("lse", lse, torch.float32, (T, H), dev)
+    if ws is not None:
+        w = _want("ws", ws, ws.dtype, ws.shape, dev)
+        n = ws.nbytes
     return _check("csa_cache_attn_fwd", LIB.csa_cache_attn_fwd(
-        h.ptr, ptr[0], cmp._ref if cmp is not None else None, raw._ref if raw is not None else None, i,
-        idx.shape[1] if idx is not None else 0, cc, sk, cu, p0, B, T, H, d, ratio, window, softmax_scale, _dtype(q),
-        ptr[1], ls, w, ws.numel() * ws.element_size() if ws is not None else 0, _stream_of(h, stream)))
+        h.ptr, _want("q", q, q.dtype, shape, dev), cmp and cmp._ref, raw and raw._ref, i, k_pad, cc, sk, cu, p0, B, T,
+        H, d, ratio, window, softmax_scale, _dtype(q), _want("out", out, q.dtype, shape, dev), ls, w, n,
+        _stream_of(h, stream)))

@@ -91,6 +91,7 @@ cache_write_kernel(CacheView c, const T* __restrict__ x_k, const T* __restrict__
                    const int32_t* __restrict__ pos0, int B, int T_cap, int64_t n_items, int* status) {
   constexpr int kChunks = D / 8;
   __shared__ float s_max[16];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31;
   const int t = kWarpItems ? lane : threadIdx.x, n_t = kWarpItems ? 32 : blockDim.x;
   const int64_t item = kWarpItems ? (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5) : blockIdx.x;
@@ -214,6 +215,7 @@ cache_read_kernel(CacheView c, const int32_t* __restrict__ cu, const int32_t* __
                   T* __restrict__ k_out, T* __restrict__ v_out, int* status) {
   constexpr int kChunks = D / 16;
   __shared__ int s_blk[kReadRows], s_row[kReadRows];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int64_t row0 = (int64_t)blockIdx.x * kReadRows;
   const int rows = (int)min((int64_t)kReadRows, T_cap - row0);
   if ((int)threadIdx.x < rows) {
@@ -261,25 +263,25 @@ cache_read_kernel(CacheView c, const int32_t* __restrict__ cu, const int32_t* __
 }
 
 template <typename T, int D>
-void write_launch(const CacheView& c, const void* x_k, const void* x_v, const int32_t* cu, const int32_t* pos0, int B,
+cudaError_t write_launch(const CacheView& c, const void* x_k, const void* x_v, const int32_t* cu, const int32_t* pos0, int B,
                   int T_cap, int* status, cudaStream_t stream) {
   const int64_t slots = ((int64_t)T_cap >> c.log_block) + 2 * (int64_t)B;
   const int64_t items = slots * c.H_kv * (c.v ? 2 : 1);
   const T* k = static_cast<const T*>(x_k);
   const T* v = static_cast<const T*>(x_v);
   if (T_cap <= 4 * (int64_t)B)
-    cache_write_kernel<T, D, true><<<(unsigned)((items + 7) / 8), kThreads, 0, stream>>>(c, k, v, cu, pos0, B, T_cap,
-                                                                                        items, status);
-  else
-    cache_write_kernel<T, D, false><<<(unsigned)items, (D / 8 << c.log_block) / kKeep, 0, stream>>>(
-        c, k, v, cu, pos0, B, T_cap, items, status);
+    return launch_after(cache_write_kernel<T, D, true>, dim3((unsigned)((items + 7) / 8)), dim3(kThreads), 0, stream,
+                        c, k, v, cu, pos0, B, T_cap, items, status);
+  return launch_after(cache_write_kernel<T, D, false>, dim3((unsigned)items), dim3((D / 8 << c.log_block) / kKeep), 0,
+                      stream, c, k, v, cu, pos0, B, T_cap, items, status);
 }
 
 template <typename T, int D>
-void read_launch(const CacheView& c, const int32_t* cu, const int32_t* pos0, int B, int T_cap, void* k_out,
+cudaError_t read_launch(const CacheView& c, const int32_t* cu, const int32_t* pos0, int B, int T_cap, void* k_out,
                  void* v_out, int* status, cudaStream_t stream) {
-  cache_read_kernel<T, D><<<(unsigned)(((int64_t)T_cap + kReadRows - 1) / kReadRows), kThreads, 0, stream>>>(
-      c, cu, pos0, B, T_cap, static_cast<T*>(k_out), static_cast<T*>(v_out), status);
+  return launch_after(cache_read_kernel<T, D>, dim3((unsigned)(((int64_t)T_cap + kReadRows - 1) / kReadRows)),
+                      dim3(kThreads), 0, stream, c, cu, pos0, B, T_cap, static_cast<T*>(k_out),
+                      static_cast<T*>(v_out), status);
 }
 
 }  // namespace
@@ -288,24 +290,20 @@ cudaError_t launch_cache_write(const CacheView& c, const void* x_k, const void* 
                                const int32_t* pos0, int B, int T_cap, bool fp32, int* status, cudaStream_t stream) {
   if (B <= 0 || T_cap <= 0) return cudaSuccess;
   if (c.d == 64)
-    fp32 ? write_launch<float, 64>(c, x_k, x_v, cu, pos0, B, T_cap, status, stream)
+    return fp32 ? write_launch<float, 64>(c, x_k, x_v, cu, pos0, B, T_cap, status, stream)
          : write_launch<__nv_bfloat16, 64>(c, x_k, x_v, cu, pos0, B, T_cap, status, stream);
-  else
-    fp32 ? write_launch<float, 128>(c, x_k, x_v, cu, pos0, B, T_cap, status, stream)
+  return fp32 ? write_launch<float, 128>(c, x_k, x_v, cu, pos0, B, T_cap, status, stream)
          : write_launch<__nv_bfloat16, 128>(c, x_k, x_v, cu, pos0, B, T_cap, status, stream);
-  return cudaGetLastError();
 }
 
 cudaError_t launch_cache_read(const CacheView& c, const int32_t* cu, const int32_t* pos0, int B, int T_cap, bool fp32,
                               void* k_out, void* v_out, int* status, cudaStream_t stream) {
   if (T_cap <= 0) return cudaSuccess;
   if (c.d == 64)
-    fp32 ? read_launch<float, 64>(c, cu, pos0, B, T_cap, k_out, v_out, status, stream)
+    return fp32 ? read_launch<float, 64>(c, cu, pos0, B, T_cap, k_out, v_out, status, stream)
          : read_launch<__nv_bfloat16, 64>(c, cu, pos0, B, T_cap, k_out, v_out, status, stream);
-  else
-    fp32 ? read_launch<float, 128>(c, cu, pos0, B, T_cap, k_out, v_out, status, stream)
+  return fp32 ? read_launch<float, 128>(c, cu, pos0, B, T_cap, k_out, v_out, status, stream)
          : read_launch<__nv_bfloat16, 128>(c, cu, pos0, B, T_cap, k_out, v_out, status, stream);
-  return cudaGetLastError();
 }
 
 }  // namespace csa

@@ -184,7 +184,7 @@ template <int D, int MT, bool kSplit, bool kShared> struct Layout {
   static constexpr int kBuf = kRing > kMerge + kSums ? kRing : kMerge + kSums;
   static constexpr int kQ = MT * (D / 16) * 32 * 16 * (kSplit ? 2 : 1);      // query fragments
   static constexpr int kRows = kBuf + kQ;                                    // rows of the next steps
-  static constexpr int kSmem = kRows + kWarps * 2 * kAhead * kStep * 4;      // three CTAs an SM fit with MT = 1
+  static constexpr int kSmem = kRows + kWarps * kAhead * kStep * 4;      // three CTAs an SM fit with MT = 1
 };
 
 // One piece of an item in the workspace: O [R][D], then m, M, l [R].
@@ -230,6 +230,7 @@ cache_attn_kernel(const CacheAttnArgs a, const Plan pl, float* __restrict__ ws_o
   const int g = lane >> 2, c = lane & 3;
   const int G = a.H / a.H_kv;
   const uint32_t buf = smem_u32(smem), qbuf = buf + L::kBuf;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // for what ran before on the stream
   asm volatile("griddepcontrol.launch_dependents;");
 
   // ---- this CTA's share of the tiles ----
@@ -302,7 +303,7 @@ cache_attn_kernel(const CacheAttnArgs a, const Plan pl, float* __restrict__ ws_o
   }
 
   const uint32_t ring = buf + warp * (kStages * L::kStage);
-  uint32_t* rows = reinterpret_cast<uint32_t*>(smem + L::kRows) + warp * (2 * kAhead * kStep);
+  uint32_t* rows = reinterpret_cast<uint32_t*>(smem + L::kRows) + warp * (kAhead * kStep);
   // lane constants of the fragment reads
   int off_k[D / 64], off_v[2];
 #pragma unroll
@@ -338,7 +339,6 @@ cache_attn_kernel(const CacheAttnArgs a, const Plan pl, float* __restrict__ ws_o
     // of this warp, a lane a key: the list and table reads of all steps are in flight together.
     auto look_up = [&](int t) {
       int pos[kAhead], blk[kAhead];
-      uint32_t* to = rows + ((t - t0) / kAhead % 2) * (kAhead * kStep) + lane;
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
         const int tt = t + i;
@@ -374,13 +374,13 @@ cache_attn_kernel(const CacheAttnArgs a, const Plan pl, float* __restrict__ ws_o
           else
             raise_status(a.status, CSA_ERR_DEVICE_BOUNDS);
         }
-        to[i * kStep] = row;
+        rows[i * kStep + lane] = row;
       }
     };
-    auto copy = [&](int t) {  // step t's codes and scales into its stage
+    auto copy = [&](int n) {  // codes and scales of step t0 + n into its stage
+      const int t = t0 + n;
       if (t < t1) {
-        const int n = t - t0;
-        const uint32_t* from = rows + (n % (2 * kAhead)) * kStep;
+        const uint32_t* from = rows + (n % kAhead) * kStep;
         const CacheView& cc = t < x.ct ? a.cmp : a.raw;
         const uint32_t st = ring + (n % kStages) * L::kStage;
         constexpr int kPerRow = D / 16, kRowsPer = 32 / kPerRow;
@@ -402,73 +402,69 @@ cache_attn_kernel(const CacheAttnArgs a, const Plan pl, float* __restrict__ ws_o
       }
       cp_async_commit();
     };
-    look_up(t0);
-    __syncwarp();
+    // the queries as product fragments, one warp a 16-row tile
+    auto take_queries = [&]() {
+      if (warp == kWarps - 1) {
+        for (int i = lane; i < R * D / 32; i += 32) s_nan[i] = 0;
+        if (lane == 0) s_nans = 0;
+      }
+      if (warp < MT) {
+        float v[2][D / 4];  // this thread's 16-element chunks c (and c + 4) of rows g, g + 8
+        float inv[2];
 #pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) copy(t0 + i);
-
-    if (warp == kWarps - 1) {
-      for (int i = lane; i < R * D / 32; i += 32) s_nan[i] = 0;
-      if (lane == 0) s_nans = 0;
-    }
-    // ---- queries as product fragments, one warp a 16-row tile ----
-    if (warp < MT) {
-      float v[2][D / 4];  // this thread's 16-element chunks c (and c + 4) of rows g, g + 8
-      float inv[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int r = warp * 16 + g + 8 * e;
-        const int qi = G > R ? 0 : r / G, h = G > R ? r : r % G;
-        const bool real = qi < x.nq && h < heads;
-        if (c == 0) {
-          s_p[r] = real ? x.p0 + qi : -1;
-          s_vis[r] = real && a.cmp.k ? (int)(((int64_t)x.p0 + qi + 1) / a.r) : 0;
-          s_out[r] = real ? (x.row0 + qi) * a.H + h0 + h : -1;
-        }
-        const T* src = static_cast<const T*>(a.q) + ((int64_t)(x.row0 + qi) * a.H + h0 + h) * D;
-        float amax = 0.f;
-#pragma unroll
-        for (int i = 0; i < D / 4; i += 4) {
-          float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (real) {
-            const T* p = src + 16 * (c + 4 * (i / 16)) + i % 16;
-            if (kSplit) {
-              f = __ldg(reinterpret_cast<const float4*>(p));
-            } else {
-              const uint2 w = __ldg(reinterpret_cast<const uint2*>(p));
-              f = make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
-            }
+        for (int e = 0; e < 2; ++e) {
+          const int r = warp * 16 + g + 8 * e;
+          const int qi = G > R ? 0 : r / G, h = G > R ? r : r % G;
+          const bool real = qi < x.nq && h < heads;
+          if (c == 0) {
+            s_p[r] = real ? x.p0 + qi : -1;
+            s_vis[r] = real && a.cmp.k ? (int)(((int64_t)x.p0 + qi + 1) / a.r) : 0;
+            s_out[r] = real ? (x.row0 + qi) * a.H + h0 + h : -1;
           }
-          v[e][i] = f.x, v[e][i + 1] = f.y, v[e][i + 2] = f.z, v[e][i + 3] = f.w;
+          const T* src = static_cast<const T*>(a.q) + ((int64_t)(x.row0 + qi) * a.H + h0 + h) * D;
+          float amax = 0.f;
+#pragma unroll
+          for (int i = 0; i < D / 4; i += 4) {
+            float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (real) {
+              const T* p = src + 16 * (c + 4 * (i / 16)) + i % 16;
+              if (kSplit) {
+                f = __ldg(reinterpret_cast<const float4*>(p));
+              } else {
+                const uint2 w = __ldg(reinterpret_cast<const uint2*>(p));
+                f = make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
+              }
+            }
+            v[e][i] = f.x, v[e][i + 1] = f.y, v[e][i + 2] = f.z, v[e][i + 3] = f.w;
+          }
+#pragma unroll
+          for (int i = 0; i < D / 4; ++i)
+            if (fabsf(v[e][i]) < INFINITY) amax = fmaxf(amax, fabsf(v[e][i]));
+          amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+          amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+          // largest element to [2^14, 2^15), as far as 2^e and 2^-e are normal numbers
+          const int ex = max((int)(__float_as_uint(amax) >> 23) - 127 - 14, -113);
+          inv[e] = a.scale < 0.f ? -pow2i(-ex) : pow2i(-ex);
+          if (c == 0) s_qf[r] = pow2i(ex);
         }
 #pragma unroll
-        for (int i = 0; i < D / 4; ++i)
-          if (fabsf(v[e][i]) < INFINITY) amax = fmaxf(amax, fabsf(v[e][i]));
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        // largest element to [2^14, 2^15), as far as 2^e and 2^-e are normal numbers
-        const int ex = max((int)(__float_as_uint(amax) >> 23) - 127 - 14, -113);
-        inv[e] = a.scale < 0.f ? -pow2i(-ex) : pow2i(-ex);
-        if (c == 0) s_qf[r] = pow2i(ex);
-      }
+        for (int ks = 0; ks < D / 16; ++ks) {
+          uint32_t hi[4], lo[4];
 #pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks) {
-        uint32_t hi[4], lo[4];
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {  // row g, first pair; row g + 8; their second pairs
-          const int e = w & 1, i = ks * 4 + (w >> 1) * 2;
-          const float f0 = v[e][i] * inv[e], f1 = v[e][i + 1] * inv[e];
-          hi[w] = pack_f16x2(f0, f1);
-          lo[w] = rest_f16x2(hi[w], f0, f1);
+          for (int w = 0; w < 4; ++w) {  // row g, first pair; row g + 8; their second pairs
+            const int e = w & 1, i = ks * 4 + (w >> 1) * 2;
+            const float f0 = v[e][i] * inv[e], f1 = v[e][i + 1] * inv[e];
+            hi[w] = pack_f16x2(f0, f1);
+            lo[w] = rest_f16x2(hi[w], f0, f1);
+          }
+          const uint32_t at = qbuf + ((warp * (D / 16) + ks) * 32 + lane) * 16;
+          asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(hi[0]), "r"(hi[1]), "r"(hi[2]), "r"(hi[3]));
+          if (kSplit)
+            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at + L::kQ / 2), "r"(lo[0]), "r"(lo[1]),
+                         "r"(lo[2]), "r"(lo[3]));
         }
-        const uint32_t at = qbuf + ((warp * (D / 16) + ks) * 32 + lane) * 16;
-        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(hi[0]), "r"(hi[1]), "r"(hi[2]), "r"(hi[3]));
-        if (kSplit)
-          asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at + L::kQ / 2), "r"(lo[0]), "r"(lo[1]),
-                       "r"(lo[2]), "r"(lo[3]));
       }
-    }
-    __syncthreads();
+    };
     float qf[MT][2], M[MT][2], l[MT][2], o[MT][D / 8][4];
     float e0 = 0.f;         // l is of 2^(t + e0 - M + kBase), e0 the first key's V exponent
     bool any_key = false, any_far = false;
@@ -476,7 +472,6 @@ cache_attn_kernel(const CacheAttnArgs a, const Plan pl, float* __restrict__ ws_o
     for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        qf[mt][e] = s_qf[mt * 16 + g + 8 * e];
         M[mt][e] = kNone;
         l[mt][e] = 0.f;
       }
@@ -484,15 +479,29 @@ cache_attn_kernel(const CacheAttnArgs a, const Plan pl, float* __restrict__ ws_o
       for (int i = 0; i < D / 8; ++i) o[mt][i][0] = o[mt][i][1] = o[mt][i][2] = o[mt][i][3] = 0.f;
     }
 
-    for (int t = t0; t < t1; ++t) {
+    // kStages - 1 rounds that only copy, then a round a step
+    for (int n = 1 - kStages; n < t1 - t0; ++n) {
+      const int next = n + kStages - 1;
       cp_async_wait<kStages - 2>();
       __syncwarp();
-      if ((t - t0) % kAhead == 0 && t + kAhead < t1) {
-        look_up(t + kAhead);
+      if (next % kAhead == 0 && t0 + next < t1) {
+        look_up(t0 + next);
         __syncwarp();
       }
-      copy(t + kStages - 1);
-      const uint32_t st = ring + ((t - t0) % kStages) * L::kStage;
+      copy(next);
+      if (n < 0) {
+        if (n == -1) {
+          take_queries();
+          __syncthreads();
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) qf[mt][e] = s_qf[mt * 16 + g + 8 * e];
+        }
+        continue;
+      }
+      const int t = t0 + n;
+      const uint32_t st = ring + (n % kStages) * L::kStage;
       const uint32_t sc = st + L::kStage - 2 * kStep * 4;
       // each key's score factor and V exponent, in place of its scales
       bool uniform, far;    // one V scale in each half of the step (a block's); a V scale far from e0
@@ -916,18 +925,11 @@ cudaError_t run(const CacheAttnArgs& a, int sm_count, cudaStream_t stream) {
   cudaError_t e = cudaFuncSetAttribute(cache_attn_kernel<T, D, MT, kShared>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
   if (e != cudaSuccess) return e;
-  cache_attn_kernel<T, D, MT, kShared><<<grid, kThreads, L::kSmem, stream>>>(a, pl, pieces, meta, far);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid, L::R / kWarps);
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;  // its launch overlaps the first kernel
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, cache_attn_join_kernel<T, D, L::R>, a, pl, (const float*)pieces, (const int4*)meta);
+  if ((e = launch_after(cache_attn_kernel<T, D, MT, kShared>, dim3(grid), dim3(kThreads), L::kSmem, stream, a, pl,
+                        pieces, meta, far)) != cudaSuccess)
+    return e;
+  return launch_after(cache_attn_join_kernel<T, D, L::R>, dim3(grid, L::R / kWarps), dim3(kThreads), 0, stream, a, pl,
+                      (const float*)pieces, (const int4*)meta);
 }
 
 template <typename T, int D>
