@@ -27,50 +27,29 @@
 // range of the scores nor that of the block scales leaves a half's range.
 #include <math.h>
 
-#include "cache.cuh"
-#include "ws_sync.cuh"
+#include "cache_attn.cuh"
 
 namespace csa {
 
 namespace {
 
-using ws::ex2;
+using namespace cache_attn;
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kStep = 32;              // keys of a warp's step
-constexpr int kTile = kStep * kWarps;  // keys of a tile
 constexpr int kAhead = 4;              // steps whose rows are looked up together
-constexpr float kBase = 7.f;           // largest weight in the products when M is exact: 2^kBase ...
-constexpr float kSlack = 8.f;          // ... and M may lag by this much (a half ends below 2^16)
-constexpr float kNone = -3e38f;        // M before the first key
-constexpr uint32_t kNoRow = 0xffffffffu;
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint4& a, uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-// The rounding error of pack_f16x2, as halves.
-__device__ __forceinline__ uint32_t rest_f16x2(uint32_t hi, float a, float b) {
-  const float2 f = f16x2_to_float2(hi);
-  return pack_f16x2(a - f.x, b - f.y);
-}
-__device__ __forceinline__ uint32_t widen_lo(uint32_t w) { return e4m3x2_to_f16x2((uint16_t)w); }
-__device__ __forceinline__ uint32_t widen_hi(uint32_t w) { return e4m3x2_to_f16x2((uint16_t)(w >> 16)); }
 __device__ __forceinline__ float lds_f(uint32_t a) {
   float v;
   asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a));
   return v;
 }
-// Exponent of a power of two.
-__device__ __forceinline__ float exponent_of(float s) { return (float)((int)(__float_as_uint(s) >> 23) - 127); }
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 v;
   asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
@@ -85,15 +64,6 @@ __device__ __forceinline__ void cp_async_4_zfill(uint32_t dst, const void* src, 
   const int n = valid ? 4 : 0;
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(dst), "l"(src), "r"(n));
 }
-// Any NaN code (0x7f with either sign) among four.
-__device__ __forceinline__ bool has_nan4(uint32_t w) { return (((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0; }
-
-// The same codes, NaN as 0.
-__device__ __forceinline__ uint32_t without_nan4(uint32_t w) {
-  const uint32_t nan = ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-  return w & ~(nan | (nan - (nan >> 7)));
-}
-
 // Byte offset of 16-byte chunk `ch` of row `row` in a 16-row tile of codes.  The
 // chunks of a 128-byte line are permuted so that the eight lanes of a 16-byte
 // read phase hit all banks: K reads take four chunks of two neighbouring rows,
@@ -122,56 +92,6 @@ __device__ __noinline__ void note_nans(uint32_t at, int hf, int first, bool entr
   __syncwarp();
 }
 
-struct Plan {  // what every CTA derives from the arguments
-  int lq;      // queries of an item: 1 << lq
-  int parts;   // items of one query group and KV head: ceil(G / R) when G > R
-  int subs;    // H_kv * parts
-  int slots;   // query groups, at most
-};
-
-struct Slot {  // a query group
-  int b, row0, nq, p0;  // sequence, first packed row, queries, position of the first
-  int ct, rt;           // tiles of compressed entries, of raw rows
-  int vis, w0;          // last query's visible entries (listed: k_pad); first raw position of the tiles
-  bool bad;
-};
-
-// Query group `s`: sequences' groups start at floor(cu / 2^lq) + b, which leaves
-// every sequence room for ceil(L / 2^lq).  nq = 0: none.
-__device__ __forceinline__ Slot find_slot(const CacheAttnArgs& a, const Plan& pl, const int32_t* cu,
-                                          const int32_t* pos0, int s) {
-  Slot r{};
-  int lo = 0, hi = a.B - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if ((cu[mid] >> pl.lq) + mid <= s) lo = mid; else hi = mid - 1;
-  }
-  const int row0 = cu[lo], L = cu[lo + 1] - row0;
-  const int64_t first = (int64_t)(s - ((row0 >> pl.lq) + lo)) << pl.lq;
-  if (first < 0 || first >= L || row0 < 0 || (int64_t)row0 + L > a.T_cap) return r;
-  r.b = lo;
-  r.row0 = row0 + (int)first;
-  r.nq = min(L - (int)first, 1 << pl.lq);
-  const int64_t end = (int64_t)pos0[lo] + L;
-  r.bad = pos0[lo] < 0 || end > INT32_MAX || (a.raw.k && end > a.raw.cap) || (a.cmp.k && end / a.r > a.cmp.cap);
-  if (r.bad) {
-    r.ct = 1;
-    return r;
-  }
-  r.p0 = pos0[lo] + (int)first;
-  const int p1 = r.p0 + r.nq - 1;
-  if (a.cmp.k) {
-    r.vis = a.idx ? a.k_pad : (int)(((int64_t)p1 + 1) / a.r);
-    r.ct = (r.vis + kTile - 1) / kTile;
-  }
-  if (a.raw.k) {
-    r.w0 = max(0, r.p0 - a.window + 1) & ~15;  // 16 keys lie in one block
-    r.rt = (p1 - r.w0) / kTile + 1;
-  }
-  if (r.ct + r.rt == 0) r.ct = 1;  // nothing in sight: the rows are still written
-  return r;
-}
-
 template <int D, int MT, bool kSplit, bool kShared> struct Layout {
   static constexpr int R = 16 * MT;
   static constexpr int kCodes = kStep * D;                                   // bytes of a step's rows
@@ -187,28 +107,6 @@ template <int D, int MT, bool kSplit, bool kShared> struct Layout {
   static constexpr int kSmem = kRows + kWarps * kAhead * kStep * 4;      // three CTAs an SM fit with MT = 1
 };
 
-// One piece of an item in the workspace: O [R][D], then m, M, l [R].
-template <int D> __host__ __device__ constexpr int piece_floats(int R) { return R * (D + 4); }
-
-// A row's result from its joined sums: four dims of it, and with the first ones its lse.
-template <typename T, int D>
-__device__ __forceinline__ void finish_row(const CacheAttnArgs& a, int at, int d4, float4 v, float m, float M, float l) {
-  if (a.sink) {  // it joins the sum and has no value row
-    const float s2 = __ldg(a.sink + at % a.H) * kLog2e, top = fmaxf(m, s2);
-    l = l * ex2(m - top) + (s2 > kNone ? ex2(s2 - top) : 0.f);
-    m = top;
-  }
-  if (M == kNone && l == l) v = make_float4(0.f, 0.f, 0.f, 0.f);  // no key in sight
-  else {
-    const float f = ex2(0.5f * (M - kBase - m)), f2 = f / l;          // 2^(M - kBase - m) in two halves
-    v.x = v.x * f * f2, v.y = v.y * f * f2, v.z = v.z * f * f2, v.w = v.w * f * f2;
-  }
-  T* out = static_cast<T*>(a.out) + (int64_t)at * D + 4 * d4;
-  if (sizeof(T) == 4) *reinterpret_cast<float4*>(out) = v;
-  else *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-  if (d4 == 0 && a.lse) a.lse[at] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
-}
-
 template <typename T, int D, int MT, bool kShared>
 __global__ void __launch_bounds__(kThreads, MT == 1 ? 3 : 2)
 cache_attn_kernel(const CacheAttnArgs a, const Plan pl, float* __restrict__ ws_o, int4* __restrict__ ws_meta,
@@ -217,9 +115,7 @@ cache_attn_kernel(const CacheAttnArgs a, const Plan pl, float* __restrict__ ws_o
   using L = Layout<D, MT, kSplit, kShared>;
   constexpr int R = L::R, kStages = L::kStages;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int64_t s_sum[kWarps];
-  __shared__ int64_t s_at;
-  __shared__ int s_slot;
+  __shared__ Context s_ctx;
   __shared__ float s_qf[R];                       // a row's query is q * 2^-e; 2^e
   __shared__ int s_p[R], s_vis[R];                // a row's position (-1: no such row), the entries that it sees
   __shared__ uint32_t s_nan[R * D / 32];          // dims of a row that a NaN reached (see note_nans)
@@ -233,74 +129,9 @@ cache_attn_kernel(const CacheAttnArgs a, const Plan pl, float* __restrict__ ws_o
   asm volatile("griddepcontrol.wait;" ::: "memory");  // for what ran before on the stream
   asm volatile("griddepcontrol.launch_dependents;");
 
-  // ---- this CTA's share of the tiles ----
-  const int32_t* cu = a.cu;
-  const int32_t* pos0 = a.pos0;
-  if ((2 * (int64_t)a.B + 1) * 4 <= L::kBuf) {  // searched by every thread: where the rings will be
-    int32_t* s_cu = reinterpret_cast<int32_t*>(smem);
-    for (int i = tid; i <= a.B; i += kThreads) {
-      s_cu[i] = __ldg(a.cu + i);
-      if (i < a.B) s_cu[a.B + 1 + i] = __ldg(a.pos0 + i);
-    }
-    __syncthreads();
-    cu = s_cu;
-    pos0 = s_cu + a.B + 1;
-  }
-  const int n_slots = a.B > 0 ? pl.slots : 0;
-  const int per = (n_slots + kThreads - 1) / kThreads;
-  const int slot0 = min(tid * per, n_slots), slot1 = min(slot0 + per, n_slots);
-  int64_t mine = 0;
-  for (int s = slot0; s < slot1; ++s) {
-    const Slot x = find_slot(a, pl, cu, pos0, s);
-    if (x.nq) mine += (int64_t)(x.ct + x.rt) * pl.subs;
-  }
-  int64_t incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
-  }
-  if (lane == 31) s_sum[warp] = incl;
-  __syncthreads();
-  int64_t total = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) incl += s_sum[w];
-    total += s_sum[w];
-  }
-  const int64_t grid = min((int64_t)gridDim.x, total);  // CTAs that get a tile or more; the rest none
-  auto share = [&](int64_t cta) { return cta >= grid ? total : total * cta / grid; };
-  const int64_t u0 = share(blockIdx.x), u1 = share((int64_t)blockIdx.x + 1);
   if (tid == 0) ws_meta[blockIdx.x] = make_int4(-1, 0, 0, 0);
-  if (u0 < u1 && incl - mine <= u0 && u0 < incl) {
-    int64_t at = incl - mine;
-    int s = slot0;
-    while (true) {
-      const Slot x = find_slot(a, pl, cu, pos0, s);
-      const int64_t n = x.nq ? (int64_t)(x.ct + x.rt) * pl.subs : 0;
-      if (u0 < at + n) break;
-      at += n;
-      ++s;
-    }
-    s_slot = s;
-    s_at = at;
-  }
-  __syncthreads();
-
-  // ---- rows that belong to no sequence ----
-  {
-    const int r0 = max(__ldg(a.cu + a.B), 0);
-    T* out = static_cast<T*>(a.out);
-    const int64_t n = ((int64_t)a.T_cap - r0) * a.H;
-    for (int64_t i = (int64_t)blockIdx.x * kThreads + tid; i < n * (D / 8); i += (int64_t)gridDim.x * kThreads) {
-      uint4* o = reinterpret_cast<uint4*>(out + (int64_t)r0 * a.H * D) + i * (sizeof(T) / 2);
-      o[0] = make_uint4(0, 0, 0, 0);
-      if (sizeof(T) == 4) o[1] = make_uint4(0, 0, 0, 0);
-    }
-    if (a.lse)
-      for (int64_t i = (int64_t)blockIdx.x * kThreads + tid; i < n; i += (int64_t)gridDim.x * kThreads)
-        a.lse[(int64_t)r0 * a.H + i] = -INFINITY;
-  }
+  split_tiles<kThreads, true>(a, pl, R, &s_ctx, smem, L::kBuf);
+  capacity_rows<T, D, kThreads>(a);
 
   const uint32_t ring = buf + warp * (kStages * L::kStage);
   uint32_t* rows = reinterpret_cast<uint32_t*>(smem + L::kRows) + warp * (kAhead * kStep);
@@ -315,24 +146,12 @@ cache_attn_kernel(const CacheAttnArgs a, const Plan pl, float* __restrict__ ws_o
   float* far_l = far_m + R;
   const float scale_log2 = fabsf(a.scale) * kLog2e;  // its sign is put into the queries
 
-  int64_t u = u0;
-  int slot = u0 < u1 ? s_slot : 0;
-  int64_t slot_at = u0 < u1 ? s_at : 0;
-  while (u < u1) {
-    // ---- the next item: query group, KV head, part of the heads, tiles [t0, t1) ----
-    const Slot x = find_slot(a, pl, a.cu, a.pos0, slot);
-    const int64_t n_tiles = x.nq ? x.ct + x.rt : 0;
-    if (u >= slot_at + n_tiles * pl.subs) {
-      slot_at += n_tiles * pl.subs;
-      ++slot;
-      continue;
-    }
-    const int sub = (int)((u - slot_at) / n_tiles);
-    const int64_t item0 = slot_at + sub * n_tiles;
-    const int t0 = (int)(u - item0), t1 = (int)min(u1 - item0, n_tiles);
-    const int kvh = sub / pl.parts, h0 = kvh * G + (sub % pl.parts) * R;
-    const int heads = min(kvh * G + G - h0, G > R ? R : G);  // heads of a query in this item
-    const int vis = x.bad || !a.cmp.k ? 0 : (int)(((int64_t)x.p0 + 1) / a.r);  // of the first query
+  Items items{s_ctx.sh.u0, s_ctx.sh.slot_at, s_ctx.sh.slot};
+  Item found;
+  while (call_next_item(&s_ctx, &items, &found)) {
+    const Item it = found;
+    const Slot& x = it.x;
+    const int t0 = it.t0, t1 = it.t1;
     if (x.bad && tid == 0) raise_status(a.status, CSA_ERR_DEVICE_BOUNDS);
 
     // Cache rows (block * H_kv + head) * block + row of the keys of steps [t, t + kAhead)
@@ -340,42 +159,14 @@ cache_attn_kernel(const CacheAttnArgs a, const Plan pl, float* __restrict__ ws_o
     auto look_up = [&](int t) {
       int pos[kAhead], blk[kAhead];
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        const int tt = t + i;
-        const int k = tt * kTile + warp * kStep + lane;
-        pos[i] = -1;
-        if (!x.bad && tt < t1) {
-          if (tt < x.ct) {
-            if (k < x.vis) pos[i] = a.idx ? __ldg(a.idx + (int64_t)x.row0 * a.k_pad + k) : k;
-          } else {
-            const int p = x.w0 + k - x.ct * kTile;
-            if (p >= x.p0 - a.window + 1 && p < x.p0 + x.nq) pos[i] = p;
-          }
-        }
-      }
+      for (int i = 0; i < kAhead; ++i) pos[i] = key_position(a, it, t + i, warp * kStep + lane);
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
-        const bool entry = t + i < x.ct;
-        if (entry && a.idx && pos[i] >= 0) {
-          const int64_t e = (int64_t)pos[i] - (a.cu_cmp ? __ldg(a.cu_cmp + x.b) : 0);
-          pos[i] = e >= 0 && e < vis ? (int)e : -1;
-          if (pos[i] < 0) raise_status(a.status, CSA_ERR_DEVICE_BOUNDS);
-        }
-        const CacheView& cc = entry ? a.cmp : a.raw;
-        blk[i] = pos[i] >= 0 ? __ldg(cc.table + (int64_t)x.b * cc.max_blocks + (pos[i] >> cc.log_block)) : 0;
+        pos[i] = checked_position(a, it, t + i, pos[i]);
+        blk[i] = table_entry(a, it, t + i, pos[i]);
       }
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        const CacheView& cc = t + i < x.ct ? a.cmp : a.raw;
-        uint32_t row = kNoRow;
-        if (pos[i] >= 0) {
-          if (blk[i] >= 0 && blk[i] < cc.n_blocks)
-            row = ((uint32_t)(blk[i] * a.H_kv + kvh) << cc.log_block) + (pos[i] & ((1 << cc.log_block) - 1));
-          else
-            raise_status(a.status, CSA_ERR_DEVICE_BOUNDS);
-        }
-        rows[i * kStep + lane] = row;
-      }
+      for (int i = 0; i < kAhead; ++i) rows[i * kStep + lane] = cache_row(a, it, t + i, pos[i], blk[i]);
     };
     auto copy = [&](int n) {  // codes and scales of step t0 + n into its stage
       const int t = t0 + n;
@@ -415,13 +206,13 @@ cache_attn_kernel(const CacheAttnArgs a, const Plan pl, float* __restrict__ ws_o
         for (int e = 0; e < 2; ++e) {
           const int r = warp * 16 + g + 8 * e;
           const int qi = G > R ? 0 : r / G, h = G > R ? r : r % G;
-          const bool real = qi < x.nq && h < heads;
+          const bool real = qi < x.nq && h < it.heads;
           if (c == 0) {
             s_p[r] = real ? x.p0 + qi : -1;
-            s_vis[r] = real && a.cmp.k ? (int)(((int64_t)x.p0 + qi + 1) / a.r) : 0;
-            s_out[r] = real ? (x.row0 + qi) * a.H + h0 + h : -1;
+            s_vis[r] = real && a.cmp.k ? (x.p0 + qi + 1) / a.r : 0;
+            s_out[r] = real ? (x.row0 + qi) * a.H + it.h0 + h : -1;
           }
-          const T* src = static_cast<const T*>(a.q) + ((int64_t)(x.row0 + qi) * a.H + h0 + h) * D;
+          const T* src = static_cast<const T*>(a.q) + ((int64_t)(x.row0 + qi) * a.H + it.h0 + h) * D;
           float amax = 0.f;
 #pragma unroll
           for (int i = 0; i < D / 4; i += 4) {
@@ -564,7 +355,7 @@ cache_attn_kernel(const CacheAttnArgs a, const Plan pl, float* __restrict__ ws_o
       const int first = t * kTile + warp * kStep + (entries ? 0 : x.w0 - x.ct * kTile);
       bool mixed = false;
       if (x.nq > 1)
-        mixed = entries ? first + kStep > vis : first + kStep - 1 > x.p0 || first <= x.p0 + x.nq - 1 - a.window;
+        mixed = entries ? first + kStep > it.vis : first + kStep - 1 > x.p0 || first <= x.p0 + x.nq - 1 - a.window;
 
       // ---- softmax: s becomes u = t + e, then the weights 2^(u - M + kBase) ----
       float ev[8];  // keys 8 j + 2 c, + 1
@@ -808,7 +599,7 @@ cache_attn_kernel(const CacheAttnArgs a, const Plan pl, float* __restrict__ ws_o
           }
       }
     __syncthreads();
-    const bool whole = t0 == 0 && t1 == n_tiles;
+    const bool whole = t0 == 0 && t1 == it.n_tiles;
     float* piece = ws_o + ((int64_t)blockIdx.x * 2 + (t0 == 0 ? 1 : 0)) * piece_floats<D>(R);
     for (int i = tid; i < R * (D / 4); i += kThreads) {
       const int r = i / (D / 4), d4 = i % (D / 4);
@@ -841,60 +632,12 @@ cache_attn_kernel(const CacheAttnArgs a, const Plan pl, float* __restrict__ ws_o
         }
         continue;
       }
-      finish_row<T, D>(a, at, d4, v, mm, MM, ll);
+      store_out<T>(a, at, D, d4, v, finish_factors(a, at, mm, MM, ll));
     }
-    if (!whole && t0 == 0 && tid == 0) {
-      // the pieces of this item: this one, then the first pieces of the CTAs up to that of its last tile
-      const int64_t last = item0 + n_tiles - 1;
-      int64_t cta = (last * grid) / total;
-      while (share(cta + 1) <= last) ++cta;
-      while (share(cta) > last) --cta;
-      ws_meta[blockIdx.x] = make_int4(x.row0, x.nq, sub, (int)cta);
-    }
+    if (!whole && t0 == 0 && tid == 0)  // its pieces: this one, then the first ones of the CTAs up to its last tile's
+      note_split(&s_ctx, x.row0, x.nq, it.sub, it.item0, it.n_tiles, ws_meta + blockIdx.x);
     __syncthreads();  // s_out, s_m and the buffers are taken again
-    u = item0 + t1;
   }
-}
-
-// Joins the pieces of the item that begins in CTA blockIdx.x's share and goes on
-// in later ones; a warp per row.
-template <typename T, int D, int R>
-__global__ void __launch_bounds__(kThreads)
-cache_attn_join_kernel(const CacheAttnArgs a, const Plan pl, const float* __restrict__ ws_o,
-                       const int4* __restrict__ ws_meta) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int4 meta = ws_meta[blockIdx.x];
-  if (meta.x < 0) return;
-  const int lane = threadIdx.x & 31, r = blockIdx.y * kWarps + (threadIdx.x >> 5);
-  const int G = a.H / a.H_kv, sub = meta.z, first = blockIdx.x, last = meta.w;
-  const int kvh = sub / pl.parts, h0 = kvh * G + (sub % pl.parts) * R;
-  const int heads = min(kvh * G + G - h0, G > R ? R : G);
-  const int qi = G > R ? 0 : r / G, h = G > R ? r : r % G;
-  if (qi >= meta.y || h >= heads) return;
-  auto piece = [&](int cta) { return ws_o + ((int64_t)cta * 2 + (cta == first ? 1 : 0)) * piece_floats<D>(R); };
-  float m = kNone, M = kNone;
-  for (int k = first + lane; k <= last; k += 32) {
-    m = fmaxf(m, piece(k)[R * D + r]);
-    M = fmaxf(M, piece(k)[R * D + R + r]);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  }
-  float l = 0.f;
-  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-  const int d4 = lane % (D / 4);
-#pragma unroll 4
-  for (int k = first; k <= last; ++k) {
-    const float* p = piece(k);
-    const float4 x = *reinterpret_cast<const float4*>(p + r * D + 4 * d4);
-    const float pm = p[R * D + r], pM = p[R * D + R + r], q = p[R * D + 2 * R + r];
-    l += q * ex2(pm - m);
-    const float f = ex2(pM - M);
-    v.x += x.x * f, v.y += x.y * f, v.z += x.z * f, v.w += x.w * f;
-  }
-  if (lane < D / 4) finish_row<T, D>(a, (meta.x + qi) * a.H + h0 + h, d4, v, m, M, l);
 }
 
 // Two row tiles a CTA where a KV head's queries fill them: more than 16 heads a
@@ -904,32 +647,27 @@ int row_tiles(int T_cap, int B, int G, bool listed, bool fp32) {
 }
 constexpr int ctas_per_sm(int mt) { return mt == 1 ? 3 : 2; }
 
-size_t ws_bytes(int sm_count, int mt, int d) {
-  const size_t grid = (size_t)sm_count * ctas_per_sm(mt);
-  return grid * (sizeof(int4) + sizeof(float) * (size_t)(16 * mt) * (2 * (d + 4) + 2 * kWarps));
-}
-
 template <typename T, int D, int MT, bool kShared>
 cudaError_t run(const CacheAttnArgs& a, int sm_count, cudaStream_t stream) {
   using L = Layout<D, MT, sizeof(T) == 4, kShared>;
-  const int G = a.H / a.H_kv;
-  Plan pl{};
-  while (!a.idx && (2 << pl.lq) * G <= L::R) ++pl.lq;
-  pl.parts = G > L::R ? (G + L::R - 1) / L::R : 1;
-  pl.subs = a.H_kv * pl.parts;
-  pl.slots = (a.T_cap >> pl.lq) + a.B;
+  const Plan pl = make_plan(a, L::R);
   const int grid = sm_count * ctas_per_sm(MT);
-  int4* meta = static_cast<int4*>(a.ws);
-  float* pieces = reinterpret_cast<float*>(meta + grid);
-  float* far = pieces + (size_t)grid * 2 * piece_floats<D>(L::R);
+  const Scratch sc = scratch_of<D>(a.ws, grid, L::R);
   cudaError_t e = cudaFuncSetAttribute(cache_attn_kernel<T, D, MT, kShared>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
   if (e != cudaSuccess) return e;
   if ((e = launch_after(cache_attn_kernel<T, D, MT, kShared>, dim3(grid), dim3(kThreads), L::kSmem, stream, a, pl,
-                        pieces, meta, far)) != cudaSuccess)
+                        sc.pieces, sc.meta, sc.far)) != cudaSuccess)
     return e;
   return launch_after(cache_attn_join_kernel<T, D, L::R>, dim3(grid, L::R / kWarps), dim3(kThreads), 0, stream, a, pl,
-                      (const float*)pieces, (const int4*)meta);
+                      (const float*)sc.pieces, (const int4*)sc.meta);
+}
+
+// Rows of an item on tcgen05 (cache_attn_tc.cu), or 0.
+int tc_rows(int T_cap, int B, int G, int d, bool listed, bool fp32) {
+  if (fp32 || d != 128) return 0;
+  if (!listed && (int64_t)T_cap > 4 * (int64_t)B) return 128;
+  return G > 64 ? 128 : G > 16 ? 64 : 0;
 }
 
 template <typename T, int D>
@@ -946,11 +684,18 @@ cudaError_t choose(const CacheAttnArgs& a, int sm_count, cudaStream_t stream) {
 
 size_t cache_attn_workspace(int sm_count, int T_cap, int H, int H_kv, int d) {
   if (T_cap <= 0) return 0;
-  return ws_bytes(sm_count, 2, d) > ws_bytes(sm_count, 1, d) ? ws_bytes(sm_count, 2, d) : ws_bytes(sm_count, 1, d);
+  size_t n = cache_attn_tc_workspace(sm_count);
+  for (int mt = 1; mt <= 2; ++mt) {
+    const size_t k = scratch_bytes(sm_count * ctas_per_sm(mt), 16 * mt, d, kWarps);
+    if (k > n) n = k;
+  }
+  return n;
 }
 
 cudaError_t launch_cache_attn(const CacheAttnArgs& a, bool fp32, int sm_count, cudaStream_t stream) {
   if (a.T_cap <= 0) return cudaSuccess;
+  const int rows = tc_rows(a.T_cap, a.B, a.H / a.H_kv, a.d, a.idx != nullptr, fp32);
+  if (rows > 0) return launch_cache_attn_tc(a, rows, sm_count, stream);
   if (a.d == 64)
     return fp32 ? choose<float, 64>(a, sm_count, stream) : choose<__nv_bfloat16, 64>(a, sm_count, stream);
   return fp32 ? choose<float, 128>(a, sm_count, stream) : choose<__nv_bfloat16, 128>(a, sm_count, stream);

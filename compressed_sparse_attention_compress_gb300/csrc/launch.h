@@ -217,5 +217,8 @@ struct CacheAttnArgs {
 };
 size_t cache_attn_workspace(int sm_count, int T_cap, int H, int H_kv, int d);
 cudaError_t launch_cache_attn(const CacheAttnArgs& a, bool fp32, int sm_count, cudaStream_t stream);
+// Its tcgen05 form (bf16, 128 dims; items of 64 or 128 rows); launch_cache_attn dispatches to it.
+size_t cache_attn_tc_workspace(int sm_count);
+cudaError_t launch_cache_attn_tc(const CacheAttnArgs& a, int rows, int sm_count, cudaStream_t stream);
 
 }  // namespace csa
