@@ -34,8 +34,8 @@ constexpr int kSoftThreads = 32 * kSoftWarps, kConvThreads = 32 * kConvWarps;
 constexpr int kMmaWarp = kSoftWarps + kConvWarps;
 constexpr int kThreads = 32 * (kMmaWarp + 4);  // whole warpgroups; two of the last one's warps have no part
 constexpr int kConvKeys = kTile / kConvWarps;  // keys of a converter warp
-// Registers a thread: 640 threads are launched with 96 each (61,440); 256 x 128 + 256 x 80 + 128 x 56 = 60,416.
-constexpr int kSoftRegs = 128, kConvRegs = 80, kMmaRegs = 56;
+// Registers a thread: 640 threads are launched with 96 each (61,440); 256 x 120 + 256 x 88 + 128 x 56 = 60,416.
+constexpr int kSoftRegs = 120, kConvRegs = 88, kMmaRegs = 56;
 constexpr int kSoftBar = 1, kConvBar = 2;   // named barriers
 constexpr int kRing = 4;                    // tiles (items) whose key factors (NaN notes) can be in use at once
 constexpr int kAhead = 4;                   // tiles whose rows are looked up together
@@ -65,6 +65,11 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int a_mn, int b_m
 
 __device__ __forceinline__ void sts128(uint32_t at, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+__device__ __forceinline__ float tmem_ld1_sync(uint32_t at) {
+  uint32_t r;
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\ntcgen05.wait::ld.sync.aligned;\n" : "=r"(r) : "r"(at) : "memory");
+  return __uint_as_float(r);
 }
 __device__ __forceinline__ void tmem_ld32f_sync(uint32_t at, float (&v)[32]) {
   uint32_t r[32];
@@ -110,23 +115,6 @@ __device__ __forceinline__ float warp_sum32(float (&v)[32], int lane) {
   return v[0];
 }
 
-// Adds a warp's 2^t, 32 rows a thread, to the rows' far sums (-inf: no term).  Rare.
-__device__ __noinline__ void add_far(const float* t, float* far_m, float* far_l, int lane) {
-  for (int j = 0; j < 32; ++j) {
-    const float old = far_m[j];
-    float top = t[j];
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    top = fmaxf(top, old);
-    float sum = t[j] > -INFINITY ? ex2(t[j] - top) : 0.f;
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) {
-      far_l[j] = far_l[j] * ex2(old - top) + sum;
-      far_m[j] = top;
-    }
-    __syncwarp();
-  }
-}
-
 // Whether some of the item's queries see a key of tile t that others do not.
 __device__ __forceinline__ bool mixed_tile(const CacheAttnArgs& a, const Item& it, int t, int& first) {
   const Slot& x = it.x;
@@ -136,26 +124,9 @@ __device__ __forceinline__ bool mixed_tile(const CacheAttnArgs& a, const Item& i
   return entries ? first + kTile > it.vis : first + kTile - 1 > x.p0 || first <= x.p0 + x.nq - 1 - a.window;
 }
 
-// Notes the rows and dims that a NaN among 16 V codes of the key at `pos` reaches: query
-// r / G at p0 + r / G sees entries below (p + 1) / ratio, or (ratio 0) the rows of its window.  Rare.
-template <int N>
-__device__ __noinline__ void note_nans(uint4 codes, int pos, int d0, int p0, int G, int ratio, int window,
-                                       uint32_t* s_nan) {
-  for (int i = 0; i < 16; ++i) {
-    const uint32_t w = i < 4 ? codes.x : i < 8 ? codes.y : i < 12 ? codes.z : codes.w;
-    if ((w >> (8 * (i % 4)) & 0x7f) != 0x7f) continue;
-    for (int r = 0; r < N; ++r) {
-      const int p = p0 + r / G;
-      if (ratio > 0 ? pos < ((int64_t)p + 1) / ratio : pos <= p && pos > p - window)
-        atomicOr(s_nan + (r * kDim + d0 + i) / 32, 1u << ((d0 + i) % 32));
-    }
-  }
-}
-
 template <int N, bool kShared>
 __global__ void __launch_bounds__(kThreads, 1)
-cache_attn_tc_kernel(const CacheAttnArgs a, const Plan pl, float* __restrict__ ws_o, int4* __restrict__ ws_meta,
-                     float* ws_far) {
+cache_attn_tc_kernel(const CacheAttnArgs a, const Plan pl, float* __restrict__ ws_o, int4* __restrict__ ws_meta) {
   using C = Tc<N, kShared>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ Context s_ctx;
@@ -175,6 +146,7 @@ cache_attn_tc_kernel(const CacheAttnArgs a, const Plan pl, float* __restrict__ w
   __shared__ float s_m[4][N], s_l[4][N];
   __shared__ int2 s_sees[2][N];                            // entries, raw rows that a row sees: first, how many
   __shared__ int s_out[N];
+  __shared__ float2 s_far[kSoftWarps][N / 2];              // reference and sum of a warp's far keys
   __shared__ int s_abort;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -305,24 +277,17 @@ cache_attn_tc_kernel(const CacheAttnArgs a, const Plan pl, float* __restrict__ w
       bool ok = mbar_wait_bounded(smem_u32(&s_qempty[qb]), (n_item / C::kQBufs & 1u) ^ 1u, status);
       float qf;
       {
-        constexpr int kIter = N * 16 / kConvThreads;
-        auto query = [&](int i, bool& real) -> const uint4* {  // chunk i of this thread: row i / 16, 8 dims
-          const int r = i >> 4, qi = G > N ? 0 : r / G, h = G > N ? r : r % G;
-          real = qi < it.x.nq && h < it.heads;
-          return reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
-                                                ((int64_t)(it.x.row0 + qi) * a.H + it.h0 + h) * kDim) + (i & 15);
+        auto query = [&](int at) -> uint4 {  // 8 dims of row at / 16
+          const int r = at >> 4, qi = G > N ? 0 : r / G, h = G > N ? r : r % G;
+          if (qi >= it.x.nq || h >= it.heads) return make_uint4(0, 0, 0, 0);
+          return __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
+                                                      ((int64_t)(it.x.row0 + qi) * a.H + it.h0 + h) * kDim) + (at & 15));
         };
         float amax = 0.f;
-        uint4 u[kIter];
-#pragma unroll
-        for (int i = 0; i < kIter; ++i) {
-          bool real;
-          const uint4* p = query(ct + i * kConvThreads, real);
-          u[i] = real ? __ldg(p) : make_uint4(0, 0, 0, 0);
-        }
-#pragma unroll
-        for (int i = 0; i < kIter; ++i) {
-          const uint32_t v[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+#pragma unroll 2
+        for (int at = ct; at < N * 16; at += kConvThreads) {
+          const uint4 u = query(at);
+          const uint32_t v[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const float x = fabsf(bf16_lo(v[j])), y = fabsf(bf16_hi(v[j]));
@@ -330,25 +295,21 @@ cache_attn_tc_kernel(const CacheAttnArgs a, const Plan pl, float* __restrict__ w
             if (y < INFINITY) amax = fmaxf(amax, y);
           }
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
         if (lane == 0) s_qmax[w] = amax;
         if ((dead = bar_or(kConvBar, kConvThreads, !ok || *abort_flag != 0))) break;
 #pragma unroll
         for (int i = 0; i < kConvWarps; ++i) amax = fmaxf(amax, s_qmax[i]);
         const int ex = max((int)(__float_as_uint(amax) >> 23) - 127 - 14, -113);
-        const float inv = a.scale < 0.f ? -pow2i(-ex) : pow2i(-ex);
+        const float mul = a.scale < 0.f ? -pow2i(-ex) : pow2i(-ex);
         qf = pow2i(ex) * fabsf(a.scale) * kLog2e;
         const uint32_t to = base + C::kQOff + qb * C::kQBytes;
-#pragma unroll
-        for (int i = 0; i < kIter; ++i) {
-          const int at = ct + i * kConvThreads;
-          const uint32_t v[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-          uint32_t f[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) f[j] = pack_f16x2(bf16_lo(v[j]) * inv, bf16_hi(v[j]) * inv);
-          const int r = at >> 4, cq = at & 15;
-          sts128(to + (cq >> 3) * C::kQRegion + tc::sw128_offset(r, cq & 7), f[0], f[1], f[2], f[3]);
+#pragma unroll 2
+        for (int at = ct; at < N * 16; at += kConvThreads) {
+          const uint4 u = query(at);
+          sts128(to + ((at & 15) >> 3) * C::kQRegion + tc::sw128_offset(at >> 4, at & 7),
+                 pack_f16x2(bf16_lo(u.x) * mul, bf16_hi(u.x) * mul), pack_f16x2(bf16_lo(u.y) * mul, bf16_hi(u.y) * mul),
+                 pack_f16x2(bf16_lo(u.z) * mul, bf16_hi(u.z) * mul), pack_f16x2(bf16_lo(u.w) * mul, bf16_hi(u.w) * mul));
         }
         tc::fence_proxy_async_smem();
         __syncwarp();
@@ -393,8 +354,15 @@ cache_attn_tc_kernel(const CacheAttnArgs a, const Plan pl, float* __restrict__ w
 #pragma unroll
             for (int i = 0; i < kChunks; ++i) {
               if (has_nan16(uv.c[i])) {
-                note_nans<N>(uv.c[i], first + kConvKeys * w + 4 * i + sub, ch * 16, it.x.p0, G > N ? N : G,
-                             t < it.x.ct ? a.r : 0, a.window, s_nan[n_item % kRing]);
+                const int pos = first + kConvKeys * w + 4 * i + sub;
+#pragma unroll 1
+                for (int j = 0; j < 16 * N; ++j) {  // dim j % 16 of the chunk, row j / 16
+                  const int d = j & 15, r = j >> 4, p = it.x.p0 + (G > N ? 0 : r / G);
+                  const uint32_t v = d < 4 ? uv.c[i].x : d < 8 ? uv.c[i].y : d < 12 ? uv.c[i].z : uv.c[i].w;
+                  if ((v >> (8 * (d & 3)) & 0x7f) == 0x7f &&
+                      (t < it.x.ct ? pos < (p + 1) / a.r : pos <= p && pos > p - a.window))
+                    atomicOr(&s_nan[n_item % kRing][(r * kDim + ch * 16 + d) / 32], 1u << ((ch * 16 + d) % 32));
+                }
                 s_nans[n_item % kRing] = 1;
                 uv.c[i] = without_nan16(uv.c[i]);
               }
@@ -519,8 +487,6 @@ cache_attn_tc_kernel(const CacheAttnArgs a, const Plan pl, float* __restrict__ w
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
     const int r0 = hh * (N / 2);  // first row of this half
     const uint32_t prow = base + C::kPOff + (N == 128 ? hh * kRegion : 0);
-    float* far_m = ws_far + ((int64_t)blockIdx.x * kSoftWarps + warp) * (2 * N);  // of N / 2 rows; then far_l
-    float* far_l = far_m + N;
     uint32_t k = 0;
     bool dead = false;
     for (uint32_t n_item = 0; !dead; ++n_item) {
@@ -645,21 +611,29 @@ cache_attn_tc_kernel(const CacheAttnArgs a, const Plan pl, float* __restrict__ w
               tc::tmem_wait_st();
             }
           }
+          if (warp_far) {  // these keys' terms go to sums in shared memory that move their own reference; rare, so not unrolled
+            if (!any_far) s_far[warp][32 * ps + lane] = make_float2(kNone, 0.f);
+            if (ps == C::kPasses - 1) any_far = true;
+            __syncwarp();
+#pragma unroll 1
+            for (int j = 0; j < 32; ++j) {
+              const int2 sees = s_sees[entries ? 0 : 1][rb + j];
+              float s = tmem_ld1_sync(t_s + j) * kq;
+              if (!far || (mixed && (uint32_t)(first + key - sees.x) >= (uint32_t)sees.y)) s = -INFINITY;
+              const float2 was = s_far[warp][32 * ps + j];
+              float high = fmaxf(s, was.x);
+#pragma unroll 1
+              for (int o = 16; o > 0; o >>= 1) high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, o));
+              float sum = ex2(s - high);
+#pragma unroll 1
+              for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+              if (lane == 0) s_far[warp][32 * ps + j] = make_float2(high, was.y * ex2(was.x - high) + sum);
+            }
+          }
           if (ps == C::kPasses - 1) {  // S^T may be overwritten
             tc::fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&s_sfree[k & 1u]));
-          }
-          if (warp_far) {
-            if (!any_far) {
-              for (int i = lane; i < N / 2; i += 32) far_m[i] = kNone, far_l[i] = 0.f;
-              __syncwarp();
-            }
-            if (ps == C::kPasses - 1) any_far = true;
-            float tt[32];
-#pragma unroll
-            for (int j = 0; j < 32; ++j) tt[j] = far && s_shift[rb + j] < kUnset ? u[j] - s_shift[rb + j] - ev : -INFINITY;
-            add_far(tt, far_m + 32 * ps, far_l + 32 * ps, lane);
           }
           // the weights: unrounded into the sums, as halves into P^T (free once the previous O^T products are done)
           if (!pv_waited && !mbar_wait_bounded(smem_u32(&s_odone), (k - 1) & 1u, status)) *abort_flag = 1;
@@ -699,8 +673,10 @@ cache_attn_tc_kernel(const CacheAttnArgs a, const Plan pl, float* __restrict__ w
         float sum = warp_sum32(l, lane);
         float m = any_key && s_M[r] > kNone ? s_M[r] - kBase - e0 : kNone;  // the sum is sum * 2^m
         if (any_far) {
-          const float fm = far_m[32 * ps + lane], top = fmaxf(m, fm);
-          sum = sum * ex2(m - top) + far_l[32 * ps + lane] * ex2(fm - top);
+          __syncwarp();
+          const float2 o = s_far[warp][32 * ps + lane];
+          const float top = fmaxf(m, o.x);
+          sum = sum * ex2(m - top) + o.y * ex2(o.x - top);
           m = top;
         }
         s_m[quad][r] = m;
@@ -736,11 +712,20 @@ cache_attn_tc_kernel(const CacheAttnArgs a, const Plan pl, float* __restrict__ w
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const int r = r0 + c0 + j, at = s_out[r];
-          float v = __uint_as_float(ro[j]) * s_f[r] * s_f2[r];
-          if (nans && (s_nan[n_item % kRing][(r * kDim + key) / 32] >> (key % 32) & 1)) v = NAN;
+          const float v = __uint_as_float(ro[j]) * s_f[r] * s_f2[r];
           if (at >= 0) {
             if (whole) static_cast<__nv_bfloat16*>(a.out)[(int64_t)at * kDim + key] = __float2bfloat16(v);
             else piece[r * kDim + key] = v;
+          }
+        }
+      }
+      if (nans) {  // what the converters took as 0
+#pragma unroll 1
+        for (int j = 0; j < N / 2; ++j) {
+          const int r = r0 + j, at = s_out[r];
+          if (at >= 0 && (s_nan[n_item % kRing][(r * kDim + key) / 32] >> (key % 32) & 1)) {
+            if (whole) static_cast<__nv_bfloat16*>(a.out)[(int64_t)at * kDim + key] = __float2bfloat16(NAN);
+            else piece[r * kDim + key] = NAN;
           }
         }
       }
@@ -776,7 +761,7 @@ cudaError_t run(const CacheAttnArgs& a, int sm_count, cudaStream_t stream) {
                                        (int)smem);
   if (e != cudaSuccess) return e;
   if ((e = launch_after(cache_attn_tc_kernel<N, kShared>, dim3(sm_count), dim3(kThreads), smem, stream, a, pl,
-                        sc.pieces, sc.meta, sc.far)) != cudaSuccess)
+                        sc.pieces, sc.meta)) != cudaSuccess)
     return e;
   return launch_after(cache_attn_join_kernel<__nv_bfloat16, kDim, N>, dim3(sm_count, N / 4), dim3(128), 0, stream, a, pl,
                       (const float*)sc.pieces, (const int4*)sc.meta);
@@ -784,7 +769,7 @@ cudaError_t run(const CacheAttnArgs& a, int sm_count, cudaStream_t stream) {
 
 }  // namespace
 
-size_t cache_attn_tc_workspace(int sm_count) { return cache_attn::scratch_bytes(sm_count, 128, kDim, kSoftWarps); }
+size_t cache_attn_tc_workspace(int sm_count) { return cache_attn::scratch_bytes(sm_count, 128, kDim, 0); }
 
 cudaError_t launch_cache_attn_tc(const CacheAttnArgs& a, int rows, int sm_count, cudaStream_t stream) {
   const bool shared = (a.cmp.k ? a.cmp.v : a.raw.v) == nullptr;
