@@ -650,7 +650,7 @@ constexpr int ctas_per_sm(int mt) { return mt == 1 ? 3 : 2; }
 template <typename T, int D, int MT, bool kShared>
 cudaError_t run(const CacheAttnArgs& a, int sm_count, cudaStream_t stream) {
   using L = Layout<D, MT, sizeof(T) == 4, kShared>;
-  const Plan pl = make_plan(a, L::R);
+  const Plan pl = make_plan(a, L::R, 1);
   const int grid = sm_count * ctas_per_sm(MT);
   const Scratch sc = scratch_of<D>(a.ws, grid, L::R);
   cudaError_t e = cudaFuncSetAttribute(cache_attn_kernel<T, D, MT, kShared>,

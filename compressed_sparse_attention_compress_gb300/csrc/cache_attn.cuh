@@ -15,7 +15,7 @@
 // scales leaves a half's range.  l = sum 2^t comes from the unrounded weights,
 // held in float32 against 2^(M - kBase - e0), e0 the first key's e.  Where an e
 // lies 60 or more from e0 that could leave float32, and the terms are summed
-// against a maximum of their own ("far", in the workspace).
+// against a maximum of their own ("far").
 #pragma once
 
 #include <math.h>
@@ -29,6 +29,7 @@ namespace cache_attn {
 using ws::ex2;
 
 constexpr int kTile = 128;             // keys of a tile
+constexpr int kManyTiles = 8;           // tiles a CTA from which the items' own cost counts in the split
 constexpr float kBase = 7.f;           // largest weight in the products when M is exact: 2^kBase ...
 constexpr float kSlack = 8.f;          // ... and M may lag by this much (a half ends below 2^16)
 constexpr float kNone = -3e38f;        // M before the first key
@@ -62,6 +63,7 @@ struct Plan {  // what every CTA derives from the arguments
   int parts;   // items of one query group and KV head: ceil(G / R) when G > R
   int subs;    // H_kv * parts
   int slots;   // query groups, at most
+  int cost;    // what an item costs beside its tiles, in tiles: queries, the first maxima, rows written
 };
 
 struct Slot {  // a query group
@@ -71,9 +73,11 @@ struct Slot {  // a query group
   bool bad;
 };
 
-struct Share {  // a CTA's tiles [u0, u1) of all `total`, and the slot that u0 lies in, which begins at slot_at
+// The order is in units: an item's `cost`, then one for each of its tiles.  Without the cost, CTAs that got the
+// many short items of a prompt's first rows ran 38% longer than the mean.
+struct Share {  // a CTA's units [u0, u1) of all `total`, and the slot that u0 lies in, which begins at slot_at
   int64_t total, grid, u0, u1, slot_at;
-  int slot;
+  int slot, cost;
   __device__ __forceinline__ int64_t of(int64_t cta) const { return cta >= grid ? total : total * cta / grid; }
 };
 
@@ -154,7 +158,7 @@ __device__ __forceinline__ void store_out(const CacheAttnArgs& a, int at, int D,
 template <int kThreads, bool kCalls>
 __device__ __forceinline__ void split_tiles(const CacheAttnArgs& a, const Plan& pl, int R, Context* ctx,
                                             uint8_t* scratch, int scratch_bytes) {
-  __shared__ int64_t s_sum[kThreads / 32];
+  __shared__ int64_t s_sum[2][kThreads / 32];
   __shared__ int64_t s_at;
   __shared__ int s_slot;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -178,27 +182,46 @@ __device__ __forceinline__ void split_tiles(const CacheAttnArgs& a, const Plan& 
   const int n_slots = a.B > 0 ? pl.slots : 0;
   const int per = (n_slots + kThreads - 1) / kThreads;
   const int slot0 = min(tid * per, n_slots), slot1 = min(slot0 + per, n_slots);
-  int64_t mine = 0;
+  int64_t mine = 0, items = 0;
   for (int s = slot0; s < slot1; ++s) {
     const Slot x = kCalls ? call_find_slot(ctx, cu, pos0, s) : find_slot(ctx, cu, pos0, s);
-    if (x.nq) mine += (int64_t)(x.ct + x.rt) * pl.subs;
+    if (x.nq) {
+      mine += (int64_t)(x.ct + x.rt) * pl.subs;
+      items += pl.subs;
+    }
   }
-  int64_t incl = mine;
+  int64_t incl = mine, incl_items = items;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
+    const int64_t v = __shfl_up_sync(0xffffffffu, incl, o), vi = __shfl_up_sync(0xffffffffu, incl_items, o);
+    if (lane >= o) {
+      incl += v;
+      incl_items += vi;
+    }
   }
-  if (lane == 31) s_sum[warp] = incl;
+  if (lane == 31) {
+    s_sum[0][warp] = incl;
+    s_sum[1][warp] = incl_items;
+  }
   __syncthreads();
   Share sh;
   sh.total = 0;
+  int64_t all_items = 0;
 #pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) incl += s_sum[w];
-    sh.total += s_sum[w];
+    if (w < warp) {
+      incl += s_sum[0][w];
+      incl_items += s_sum[1][w];
+    }
+    sh.total += s_sum[0][w];
+    all_items += s_sum[1][w];
   }
-  sh.grid = min((int64_t)gridDim.x, sh.total);  // CTAs that get a tile or more; the rest none
+  // with few tiles a CTA the longest share is what counts, in tiles
+  sh.cost = sh.total >= (int64_t)kManyTiles * gridDim.x ? pl.cost : 0;
+  sh.total += sh.cost * all_items;
+  mine += sh.cost * items;
+  incl += sh.cost * incl_items;
+  sh.grid = min((int64_t)gridDim.x, sh.total);  // CTAs that get a unit or more; the rest none
   sh.u0 = sh.of(blockIdx.x);
   sh.u1 = sh.of((int64_t)blockIdx.x + 1);
   if (sh.u0 < sh.u1 && incl - mine <= sh.u0 && sh.u0 < incl) {
@@ -206,7 +229,7 @@ __device__ __forceinline__ void split_tiles(const CacheAttnArgs& a, const Plan& 
     int s = slot0;
     while (true) {
       const Slot x = kCalls ? call_find_slot(ctx, cu, pos0, s) : find_slot(ctx, cu, pos0, s);
-      const int64_t n = x.nq ? (int64_t)(x.ct + x.rt) * pl.subs : 0;
+      const int64_t n = x.nq ? (int64_t)(x.ct + x.rt + sh.cost) * pl.subs : 0;
       if (sh.u0 < at + n) break;
       at += n;
       ++s;
@@ -241,25 +264,26 @@ __device__ __forceinline__ bool next_item(const Context* ctx, Items* st, Item* o
   const CacheAttnArgs& a = ctx->a;
   const int R = ctx->R, parts = ctx->pl.parts, subs = ctx->pl.subs, G = a.H / a.H_kv;
   while (st->u < ctx->sh.u1) {
-    Item it;
+    Item& it = *out;
     it.x = kCalls ? call_find_slot(ctx, a.cu, a.pos0, st->slot) : find_slot(ctx, a.cu, a.pos0, st->slot);
     it.n_tiles = it.x.nq ? it.x.ct + it.x.rt : 0;
-    const int64_t n = (int64_t)it.n_tiles * subs;
+    const int cost = ctx->sh.cost, units = it.x.nq ? it.n_tiles + cost : 0;
+    const int64_t n = (int64_t)units * subs;
     if (st->u >= st->slot_at + n) {
       st->slot_at += n;
       ++st->slot;
       continue;
     }
-    it.sub = (int)((st->u - st->slot_at) / it.n_tiles);
-    it.item0 = st->slot_at + (int64_t)it.sub * it.n_tiles;
-    it.t0 = (int)(st->u - it.item0);
+    it.sub = (int)((st->u - st->slot_at) / units);
+    it.item0 = st->slot_at + (int64_t)it.sub * units + cost;
+    it.t0 = (int)max(st->u - it.item0, (int64_t)0);
     it.t1 = (int)min(ctx->sh.u1 - it.item0, (int64_t)it.n_tiles);
+    if (it.t1 <= 0) break;  // the share ends before its first tile
     it.kvh = it.sub / parts;
     it.h0 = it.kvh * G + (it.sub % parts) * R;
     it.heads = min(it.kvh * G + G - it.h0, G > R ? R : G);
     it.vis = it.x.bad || !a.cmp.k ? 0 : (it.x.p0 + 1) / a.r;
     st->u = it.item0 + it.t1;
-    *out = it;
     return true;
   }
   return false;
@@ -372,13 +396,14 @@ cache_attn_join_kernel(const CacheAttnArgs a, const Plan pl, const float* __rest
 }
 
 // A CTA holds 2^lq queries of G heads, or a part of a query's heads.
-inline Plan make_plan(const CacheAttnArgs& a, int R) {
+inline Plan make_plan(const CacheAttnArgs& a, int R, int cost) {
   const int G = a.H / a.H_kv;
   Plan pl{};
   while (!a.idx && (2 << pl.lq) * G <= R) ++pl.lq;
   pl.parts = G > R ? (G + R - 1) / R : 1;
   pl.subs = a.H_kv * pl.parts;
   pl.slots = (a.T_cap >> pl.lq) + a.B;
+  pl.cost = cost;
   return pl;
 }
 

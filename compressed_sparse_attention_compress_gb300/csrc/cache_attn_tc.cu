@@ -11,11 +11,16 @@
 // Roles, one CTA per SM:
 //   8 converter warps: look rows up (list, table), load a tile's codes into registers
 //     while the one before is in use, widen them to halves (exact) into swizzled
-//     operand tiles, and leave each key's score factor and V exponent beside them;
-//   1 warp issues the products: S^T of the next tile before O^T of the current one;
+//     operand tiles, K a tile ahead of V, and leave each key's score factor and V
+//     exponent beside them; they meet only at mbarriers;
+//   1 warp issues S^T, 1 warp O^T: one issuer in one order had each product wait for
+//     what the other one waits for (prompt chunks 494 us, with two issuers 452 us);
 //   1 warp finds the CTA's items ahead of their use;
-//   8 softmax warps: (key, half of the rows); weights as halves into P^T, the sums
-//     per row in registers (reduced over keys once per item).
+//   8 softmax warps: (key, half of the rows); weights as halves into P^T, the sums per
+//     row in registers, with 128 rows in tensor memory (reduced over keys once per item).
+// Twice as many softmax warps with a quarter of the rows each were slower (dense decode
+// 66 against 57 us, prompt chunks 612 against 455 us), and so were two softmax groups that
+// take the tiles in turn: the kernel then waits for code more than for products.
 // The query rows of an item are scaled by one power of two, the largest element to
 // [2^14, 2^15): exact as halves down to 2^-32 of it.
 #include "cache_attn.cuh"
@@ -32,11 +37,11 @@ constexpr int kDim = 128;
 constexpr int kSoftWarps = 8, kConvWarps = 8;
 constexpr int kSoftThreads = 32 * kSoftWarps, kConvThreads = 32 * kConvWarps;
 constexpr int kMmaWarp = kSoftWarps + kConvWarps;
-constexpr int kThreads = 32 * (kMmaWarp + 4);  // whole warpgroups; two of the last one's warps have no part
+constexpr int kThreads = 32 * (kMmaWarp + 4);  // whole warpgroups; one of the last one's warps has no part
 constexpr int kConvKeys = kTile / kConvWarps;  // keys of a converter warp
 // Registers a thread: 640 threads are launched with 96 each (61,440); 256 x 120 + 256 x 88 + 128 x 56 = 60,416.
 constexpr int kSoftRegs = 120, kConvRegs = 88, kMmaRegs = 56;
-constexpr int kSoftBar = 1, kConvBar = 2;   // named barriers
+constexpr int kSoftBar = 1, kHalfBar = 2;  // named barriers; the last and the next one: half of the rows each
 constexpr int kRing = 4;                    // tiles (items) whose key factors (NaN notes) can be in use at once
 constexpr int kAhead = 4;                   // tiles whose rows are looked up together
 constexpr float kUnset = 1e9f;              // a row's shift before its first key: any score then asks for a maximum
@@ -133,13 +138,13 @@ cache_attn_tc_kernel(const CacheAttnArgs a, const Plan pl, float* __restrict__ w
   __shared__ uint32_t s_tmem;
   __shared__ __align__(8) uint64_t s_kfull[C::kStK], s_kempty[C::kStK], s_vfull[2], s_vempty[2], s_qfull[2],
       s_qempty[2], s_sfull[2], s_sfree[2], s_par_full[kRing], s_ifull[kRing], s_iempty[kRing],
-      s_pfull, s_odone, s_ofree, s_drain;
+      s_pfull, s_odone, s_ofree, s_drain[2], s_qmaxed;
   __shared__ Item s_item[kRing];                           // t1 < 0: no more
   __shared__ __align__(8) float2 s_par[kRing][kTile];      // score factor, V exponent (-inf: no key)
   __shared__ uint32_t s_rows[kConvWarps][2 * kAhead][kConvKeys];  // cache rows of the next tiles
   __shared__ uint32_t s_nan[kRing][N * kDim / 32];         // dims of a row that a NaN reached, by item
   __shared__ int s_nans[kRing];
-  __shared__ float s_qmax[kConvWarps];
+  __shared__ float s_qmax[2][kConvWarps];
   __shared__ __align__(16) float s_shift[N];               // kBase - M
   __shared__ float s_M[N], s_alpha[N], s_f[N], s_f2[N];
   __shared__ int s_wmax[4][64];
@@ -171,13 +176,15 @@ cache_attn_tc_kernel(const CacheAttnArgs a, const Plan pl, float* __restrict__ w
     for (int i = 0; i < kRing; ++i) {
       mbar_init(smem_u32(&s_par_full[i]), kConvWarps);
       mbar_init(smem_u32(&s_ifull[i]), 1);
-      mbar_init(smem_u32(&s_iempty[i]), kConvWarps + kSoftWarps + 1);
+      mbar_init(smem_u32(&s_iempty[i]), kConvWarps + kSoftWarps + 2);
       s_nans[i] = 0;
     }
     mbar_init(smem_u32(&s_pfull), kSoftWarps);
     mbar_init(smem_u32(&s_odone), 1);
+    mbar_init(smem_u32(&s_qmaxed), kConvWarps);
     mbar_init(smem_u32(&s_ofree), kSoftWarps);
-    mbar_init(smem_u32(&s_drain), 1);
+    mbar_init(smem_u32(&s_drain[0]), 1);
+    mbar_init(smem_u32(&s_drain[1]), 1);
     fence_mbar_init();
     s_abort = 0;
     ws_meta[blockIdx.x] = make_int4(-1, 0, 0, 0);
@@ -207,7 +214,7 @@ cache_attn_tc_kernel(const CacheAttnArgs a, const Plan pl, float* __restrict__ w
     uint32_t k = 0;                                  // eight lanes' stores then fall into different banks
     bool dead = false;
     for (uint32_t n_item = 0; !dead; ++n_item) {
-      if ((dead = bar_or(kConvBar, kConvThreads, !item_ready(n_item) || *abort_flag != 0))) break;
+      if ((dead = __any_sync(0xffffffffu, !item_ready(n_item) || *abort_flag != 0))) break;
       const Item& it = s_item[n_item % kRing];
       if (it.t1 < 0) break;
       if (it.x.bad && ct == 0) raise_status(status, CSA_ERR_DEVICE_BOUNDS);
@@ -296,10 +303,14 @@ cache_attn_tc_kernel(const CacheAttnArgs a, const Plan pl, float* __restrict__ w
           }
         }
         amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
-        if (lane == 0) s_qmax[w] = amax;
-        if ((dead = bar_or(kConvBar, kConvThreads, !ok || *abort_flag != 0))) break;
+        if (lane == 0) {
+          s_qmax[n_item & 1u][w] = amax;
+          mbar_arrive(smem_u32(&s_qmaxed));
+        }
+        ok = ok && mbar_wait_bounded(smem_u32(&s_qmaxed), n_item & 1u, status);
+        if ((dead = __any_sync(0xffffffffu, !ok))) break;
 #pragma unroll
-        for (int i = 0; i < kConvWarps; ++i) amax = fmaxf(amax, s_qmax[i]);
+        for (int i = 0; i < kConvWarps; ++i) amax = fmaxf(amax, s_qmax[n_item & 1u][i]);
         const int ex = max((int)(__float_as_uint(amax) >> 23) - 127 - 14, -113);
         const float mul = a.scale < 0.f ? -pow2i(-ex) : pow2i(-ex);
         qf = pow2i(ex) * fabsf(a.scale) * kLog2e;
@@ -311,21 +322,18 @@ cache_attn_tc_kernel(const CacheAttnArgs a, const Plan pl, float* __restrict__ w
                  pack_f16x2(bf16_lo(u.x) * mul, bf16_hi(u.x) * mul), pack_f16x2(bf16_lo(u.y) * mul, bf16_hi(u.y) * mul),
                  pack_f16x2(bf16_lo(u.z) * mul, bf16_hi(u.z) * mul), pack_f16x2(bf16_lo(u.w) * mul, bf16_hi(u.w) * mul));
         }
-        tc::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&s_qfull[qb]));
       }
 
-      for (int t = t0; t < t1; ++t) {  // the next tile's codes are loaded as soon as this one's are stored
-        int first;
-        const bool mixed = mixed_tile(a, it, t, first);
-        const int n = t - t0;
-        if (n % kAhead == 0 && t + kAhead < t1) look_up(t + kAhead);
+      // the next tile's codes are loaded as soon as this one's are stored
+      auto put_k = [&](int t, uint32_t k) {
         const uint32_t st = k % C::kStK;
-        bool good = mbar_wait_bounded(smem_u32(&s_kempty[st]), (k / C::kStK & 1u) ^ 1u, status);
-        if ((dead = bar_or(kConvBar, kConvThreads, !good || *abort_flag != 0))) break;
+        ok = mbar_wait_bounded(smem_u32(&s_kempty[st]), (k / C::kStK & 1u) ^ 1u, status);
+        if ((dead = __any_sync(0xffffffffu, !ok || *abort_flag != 0))) return;
         float ev = uk.ks > 0.f ? exponent_of(kShared ? uk.ks : uk.vs) : -INFINITY;
-        if (kShared && mixed) {  // a NaN that only some queries see: its key's scores become NaN, its values 0
+        int first;
+        if (kShared && mixed_tile(a, it, t, first)) {  // a NaN that only some queries see: its key's scores become NaN, its values 0
           uint32_t rows = 0;
 #pragma unroll
           for (int i = 0; i < kChunks; ++i) {
@@ -339,44 +347,52 @@ cache_attn_tc_kernel(const CacheAttnArgs a, const Plan pl, float* __restrict__ w
         }
         if (lane < kConvKeys) s_par[k % kRing][kConvKeys * w + lane] = make_float2(uk.ks * qf, ev);
         store(uk, base + st * kTileBytes);
-        tc::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(smem_u32(&s_par_full[k % kRing]));
           mbar_arrive(smem_u32(&s_kfull[st]));
         }
         load(uk, t + 1, false);
-        if (!kShared) {
-          const uint32_t sv = k & 1u;
-          good = mbar_wait_bounded(smem_u32(&s_vempty[sv]), (k >> 1 & 1u) ^ 1u, status);
-          if ((dead = bar_or(kConvBar, kConvThreads, !good || *abort_flag != 0))) break;
-          if (mixed) {
+      };
+      auto put_v = [&](int t, uint32_t k) {
+        const uint32_t sv = k & 1u;
+        ok = mbar_wait_bounded(smem_u32(&s_vempty[sv]), (k >> 1 & 1u) ^ 1u, status);
+        if ((dead = __any_sync(0xffffffffu, !ok || *abort_flag != 0))) return;
+        int first;
+        if (mixed_tile(a, it, t, first)) {  // such a NaN in V: noted for the rows that see it, and taken as 0
 #pragma unroll
-            for (int i = 0; i < kChunks; ++i) {
-              if (has_nan16(uv.c[i])) {
-                const int pos = first + kConvKeys * w + 4 * i + sub;
+          for (int i = 0; i < kChunks; ++i) {
+            if (has_nan16(uv.c[i])) {
+              const int pos = first + kConvKeys * w + 4 * i + sub;
 #pragma unroll 1
-                for (int j = 0; j < 16 * N; ++j) {  // dim j % 16 of the chunk, row j / 16
-                  const int d = j & 15, r = j >> 4, p = it.x.p0 + (G > N ? 0 : r / G);
-                  const uint32_t v = d < 4 ? uv.c[i].x : d < 8 ? uv.c[i].y : d < 12 ? uv.c[i].z : uv.c[i].w;
-                  if ((v >> (8 * (d & 3)) & 0x7f) == 0x7f &&
-                      (t < it.x.ct ? pos < (p + 1) / a.r : pos <= p && pos > p - a.window))
-                    atomicOr(&s_nan[n_item % kRing][(r * kDim + ch * 16 + d) / 32], 1u << ((ch * 16 + d) % 32));
-                }
-                s_nans[n_item % kRing] = 1;
-                uv.c[i] = without_nan16(uv.c[i]);
+              for (int j = 0; j < 16 * N; ++j) {  // dim j % 16 of the chunk, row j / 16
+                const int d = j & 15, r = j >> 4, p = it.x.p0 + (G > N ? 0 : r / G);
+                const uint32_t v = d < 4 ? uv.c[i].x : d < 8 ? uv.c[i].y : d < 12 ? uv.c[i].z : uv.c[i].w;
+                if ((v >> (8 * (d & 3)) & 0x7f) == 0x7f &&
+                    (t < it.x.ct ? pos < (p + 1) / a.r : pos <= p && pos > p - a.window))
+                  atomicOr(&s_nan[n_item % kRing][(r * kDim + ch * 16 + d) / 32], 1u << ((ch * 16 + d) % 32));
               }
+              s_nans[n_item % kRing] = 1;
+              uv.c[i] = without_nan16(uv.c[i]);
             }
-            __syncwarp();
           }
-          store(uv, base + C::kVOff + sv * kTileBytes);
-          tc::fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&s_vfull[sv]));
-          load(uv, t + 1, true);
         }
-        ++k;
+        store(uv, base + C::kVOff + sv * kTileBytes);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&s_vfull[sv]));
+        load(uv, t + 1, true);
+      };
+      if (!kShared) put_k(t0, k);
+      for (int t = t0; t < t1 && !dead; ++t, ++k) {
+        if ((t - t0) % kAhead == 0 && t + kAhead < t1) look_up(t + kAhead);
+        if (kShared) {
+          put_k(t, k);
+        } else {  // K a tile ahead of V: S^T of the next tile does not wait for room for this one's V
+          if (t + 1 < t1) put_k(t + 1, k + 1);
+          if (!dead) put_v(t, k);
+        }
       }
+      if (dead) break;
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&s_iempty[n_item % kRing]));
     }
@@ -385,85 +401,79 @@ cache_attn_tc_kernel(const CacheAttnArgs a, const Plan pl, float* __restrict__ w
     // =================== products ===================
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMmaRegs));
     if (warp == kMmaWarp && lane == 0) {
-      constexpr uint32_t kIdQK = idesc_f16(kTile, N, 0, 0), kIdPV = idesc_f16(kDim, N, 1, 1);
+      // S^T
+      constexpr uint32_t kId = idesc_f16(kTile, N, 0, 0);
       const uint64_t dk0 = tc::smem_desc_sw128(base, 16, 1024);
       const uint64_t dq0 = tc::smem_desc_sw128(base + C::kQOff, 16, 1024);
-      const uint64_t dv0 = tc::smem_desc_sw128(base + (kShared ? 0 : C::kVOff), kRegion, 1024);
-      const uint64_t dp = tc::smem_desc_sw128(base + C::kPOff, N == 64 ? 1024 : kRegion, 1024);
-      int t = 0, t1 = 0;        // the next tile whose S^T is issued is tile t of an item that ends at t1
-      uint32_t n_item = 0;      // items begun
-      bool first = false, last = false, ok = true;
-      auto advance = [&]() -> bool {
-        first = t == t1;
+      int t = 0, t1 = 0;
+      uint32_t n = 0;  // items begun
+      bool ok = true;
+      for (uint32_t k = 0; *abort_flag == 0; ++k) {
+        const bool first = t == t1;
         if (first) {
-          ok = ok && item_ready(n_item);
-          if (!ok) return false;
-          const Item& it = s_item[n_item % kRing];
-          t = it.t0;
-          t1 = it.t1;
-          mbar_arrive(smem_u32(&s_iempty[n_item % kRing]));
-          ++n_item;
-          if (t1 < 0) return false;
+          if (!(ok = item_ready(n))) break;
+          t = s_item[n % kRing].t0;
+          t1 = s_item[n % kRing].t1;
+          mbar_arrive(smem_u32(&s_iempty[n % kRing]));
+          ++n;
+          if (t1 < 0) break;
         }
         ++t;
-        last = t == t1;
-        return true;
-      };
-      uint32_t nq = 0, np = 0, p_items = 0;  // products issued; items begun by PV
-      auto issue_qk = [&]() {
-        const uint32_t st = nq % C::kStK, qi = n_item - 1, qb = qi % C::kQBufs;
-        ok = ok && mbar_wait_bounded(smem_u32(&s_kfull[st]), nq / C::kStK & 1u, status);
-        if (first) ok = ok && mbar_wait_bounded(smem_u32(&s_qfull[qb]), qi / C::kQBufs & 1u, status);
-        if (nq >= 2) ok = ok && mbar_wait_bounded(smem_u32(&s_sfree[nq & 1u]), ((nq >> 1) - 1) & 1u, status);
-        if (!ok || *abort_flag) return;
+        const uint32_t st = k % C::kStK, qb = (n - 1) % C::kQBufs, g = k & 1u;
+        ok = mbar_wait_bounded(smem_u32(&s_kfull[st]), k / C::kStK & 1u, status);
+        if (first) ok = ok && mbar_wait_bounded(smem_u32(&s_qfull[qb]), (n - 1) / C::kQBufs & 1u, status);
+        if (k >= 2) ok = ok && mbar_wait_bounded(smem_u32(&s_sfree[g]), ((k >> 1) - 1) & 1u, status);
+        if (!ok) break;
         tc::fence_after_sync();
+        tc::fence_proxy_async_smem();  // for the tiles' and P^T's plain stores, which the barriers made visible here
         const uint64_t dk = dk0 + ((st * kTileBytes) >> 4), dq = dq0 + ((qb * C::kQBytes) >> 4);
 #pragma unroll
         for (int ks = 0; ks < kDim / 16; ++ks)
-          tc::mma_bf16(tmem + (nq & 1u) * N, dk + (((ks >> 2) * kRegion + (ks & 3) * 32) >> 4),
-                       dq + (((ks >> 2) * C::kQRegion + (ks & 3) * 32) >> 4), kIdQK, ks > 0 ? 1u : 0u);
-        tc::mma_commit(smem_u32(&s_sfull[nq & 1u]));
+          tc::mma_bf16(tmem + g * N, dk + (((ks >> 2) * kRegion + (ks & 3) * 32) >> 4),
+                       dq + (((ks >> 2) * C::kQRegion + (ks & 3) * 32) >> 4), kId, ks > 0 ? 1u : 0u);
+        tc::mma_commit(smem_u32(&s_sfull[g]));
         if (!kShared) tc::mma_commit(smem_u32(&s_kempty[st]));
-        if (last) tc::mma_commit(smem_u32(&s_qempty[qb]));
-        ++nq;
-      };
-      auto issue_pv = [&](bool begin) {
-        ok = ok && mbar_wait_bounded(smem_u32(&s_pfull), np & 1u, status);
-        if (!kShared) ok = ok && mbar_wait_bounded(smem_u32(&s_vfull[np & 1u]), np >> 1 & 1u, status);
-        if (begin && p_items > 0) ok = ok && mbar_wait_bounded(smem_u32(&s_ofree), (p_items - 1) & 1u, status);
-        if (!ok || *abort_flag) return;
-        if (begin) ++p_items;
+        if (t == t1) tc::mma_commit(smem_u32(&s_qempty[qb]));
+      }
+      if (!ok) *abort_flag = 1;
+      tc::mma_commit(smem_u32(&s_drain[0]));  // every product has completed before tensor memory is freed
+      mbar_wait_bounded(smem_u32(&s_drain[0]), 0, status);
+    } else if (warp == kMmaWarp + 2 && lane == 0) {
+      // O^T; an issuer of its own, because in one order with S^T each waits for what the other waits for
+      constexpr uint32_t kId = idesc_f16(kDim, N, 1, 1);
+      const uint64_t dv0 = tc::smem_desc_sw128(base + (kShared ? 0 : C::kVOff), kRegion, 1024);
+      const uint64_t dp = tc::smem_desc_sw128(base + C::kPOff, N == 64 ? 1024 : kRegion, 1024);
+      int t = 0, t1 = 0;
+      uint32_t n = 0;  // items begun
+      bool ok = true;
+      for (uint32_t k = 0; *abort_flag == 0; ++k) {
+        const bool first = t == t1;
+        if (first) {
+          if (!(ok = item_ready(n))) break;
+          t = s_item[n % kRing].t0;
+          t1 = s_item[n % kRing].t1;
+          mbar_arrive(smem_u32(&s_iempty[n % kRing]));
+          ++n;
+          if (t1 < 0) break;
+        }
+        ++t;
+        const uint32_t st = kShared ? k % C::kStK : k & 1u;
+        ok = mbar_wait_bounded(smem_u32(&s_pfull), k & 1u, status);
+        if (!kShared) ok = ok && mbar_wait_bounded(smem_u32(&s_vfull[st]), k >> 1 & 1u, status);
+        if (first && n > 1) ok = ok && mbar_wait_bounded(smem_u32(&s_ofree), (n - 2) & 1u, status);  // O^T has been read
+        if (!ok) break;
         tc::fence_after_sync();
-        const uint32_t st = kShared ? np % C::kStK : np & 1u;
+        tc::fence_proxy_async_smem();  // for the tiles' and P^T's plain stores, which the barriers made visible here
         const uint64_t dv = dv0 + ((st * kTileBytes) >> 4);
 #pragma unroll
         for (int ks = 0; ks < kTile / 16; ++ks)
-          tc::mma_bf16(tmem + 2 * N, dv + ((ks * 2048) >> 4), dp + ((ks * 2048) >> 4), kIdPV,
-                       begin && ks == 0 ? 0u : 1u);
+          tc::mma_bf16(tmem + 2 * N, dv + ((ks * 2048) >> 4), dp + ((ks * 2048) >> 4), kId, first && ks == 0 ? 0u : 1u);
         tc::mma_commit(smem_u32(&s_odone));
         tc::mma_commit(kShared ? smem_u32(&s_kempty[st]) : smem_u32(&s_vempty[st]));
-        ++np;
-      };
-      // S^T of a tile before O^T of the one before it; with one query buffer the next item's
-      // queries arrive only after this item's last S^T was read, so there O^T comes first
-      bool pending = false, begin = false;  // a tile whose O^T is due; it begins an item
-      while (ok && !*abort_flag) {
-        const bool more = advance();
-        const bool late = C::kQBufs == 1 && pending && more && first;
-        for (int half = 0; half < 2; ++half) {
-          if ((half == 0) == late) {
-            if (pending) issue_pv(begin);
-          } else if (more) {
-            issue_qk();
-          }
-        }
-        pending = more;
-        begin = first;
-        if (!more) break;
       }
       if (!ok) *abort_flag = 1;
-      tc::mma_commit(smem_u32(&s_drain));  // every product has completed before tensor memory is freed
-      mbar_wait_bounded(smem_u32(&s_drain), 0, status);
+      tc::mma_commit(smem_u32(&s_drain[1]));
+      mbar_wait_bounded(smem_u32(&s_drain[1]), 0, status);
     } else if (warp == kMmaWarp + 1 && lane == 0) {
       // =================== the CTA's items, found ahead of their use ===================
       Items items{s_ctx.sh.u0, s_ctx.sh.slot_at, s_ctx.sh.slot};
@@ -472,10 +482,8 @@ cache_attn_tc_kernel(const CacheAttnArgs a, const Plan pl, float* __restrict__ w
           *abort_flag = 1;
           break;
         }
-        Item found;
-        const bool more = next_item<false>(&s_ctx, &items, &found);
-        if (!more) found.t1 = -1;
-        s_item[n % kRing] = found;
+        const bool more = next_item<false>(&s_ctx, &items, &s_item[n % kRing]);
+        if (!more) s_item[n % kRing].t1 = -1;
         mbar_arrive(smem_u32(&s_ifull[n % kRing]));
         if (!more) break;
       }
@@ -562,7 +570,7 @@ cache_attn_tc_kernel(const CacheAttnArgs a, const Plan pl, float* __restrict__ w
 #pragma unroll
           for (int j = 1; j < 32; ++j) top = fmaxf(top, u[j]);
           const bool bad = !good || *abort_flag != 0;
-          if (bar_or(kSoftBar, kSoftThreads, top > kBase + kSlack || bad)) {
+          if (bar_or(kHalfBar + hh, kSoftThreads / 2, top > kBase + kSlack || bad)) {
             // the references move to the maxima over the tile's keys
             {
               uint32_t rs[32];
@@ -578,22 +586,22 @@ cache_attn_tc_kernel(const CacheAttnArgs a, const Plan pl, float* __restrict__ w
             bool done = true;
             if (!pv_waited) done = mbar_wait_bounded(smem_u32(&s_odone), (k - 1) & 1u, status);
             pv_waited = true;
-            if (bar_or(kSoftBar, kSoftThreads, bad || !done)) {
+            if (bar_or(kHalfBar + hh, kSoftThreads / 2, bad || !done)) {
               dead = true;
               break;
             }
             tc::fence_after_sync();
-            if (tid < 64) {
-              const int r = (tid >> 5) * (N / 2) + 32 * ps + (tid & 31);
+            if (quad == 0) {
+              const int r = rb + lane;
               const float old = s_M[r];
               float v = old;
 #pragma unroll
-              for (int q = 0; q < 4; ++q) v = fmaxf(v, float_of(s_wmax[q][tid]));
+              for (int q = 0; q < 4; ++q) v = fmaxf(v, float_of(s_wmax[q][hh * 32 + lane]));
               s_alpha[r] = ex2(old - v);
               s_M[r] = v;
               s_shift[r] = v == kNone ? kUnset : kBase - v;
             }
-            bar_sync(kSoftBar, kSoftThreads);
+            bar_sync(kHalfBar + hh, kSoftThreads / 2);
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
               u[j] += s_shift[rb + j];
@@ -655,15 +663,13 @@ cache_attn_tc_kernel(const CacheAttnArgs a, const Plan pl, float* __restrict__ w
           if (C::kPasses > 1) tmem_st32f(t_l, l);
         }
         if (dead) break;
-        tc::fence_proxy_async_smem();
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&s_pfull));
       }
-      if (!dead) {  // ---- the item's rows ----
-        const bool done = mbar_wait_bounded(smem_u32(&s_odone), (k - 1) & 1u, status);
-        dead = bar_or(kSoftBar, kSoftThreads, !done || *abort_flag != 0);
-      }
+      // ---- the item's rows ----
+      const bool done = !dead && mbar_wait_bounded(smem_u32(&s_odone), (k - 1) & 1u, status);
+      dead = bar_or(kSoftBar, kSoftThreads, !done || *abort_flag != 0);
       if (dead) break;
       tc::fence_after_sync();
 #pragma unroll 1
@@ -754,7 +760,8 @@ cache_attn_tc_kernel(const CacheAttnArgs a, const Plan pl, float* __restrict__ w
 template <int N, bool kShared>
 cudaError_t run(const CacheAttnArgs& a, int sm_count, cudaStream_t stream) {
   using C = Tc<N, kShared>;
-  const Plan pl = make_plan(a, N);
+  // an item costs as much as 2 or 4 tiles beside its own (prompt chunks: 444 us with 0, 399 us so)
+  const Plan pl = make_plan(a, N, N == 128 ? 2 : 4);
   const Scratch sc = scratch_of<kDim>(a.ws, sm_count, N);
   const size_t smem = C::kSmem + 1024;
   cudaError_t e = cudaFuncSetAttribute(cache_attn_tc_kernel<N, kShared>, cudaFuncAttributeMaxDynamicSharedMemorySize,
