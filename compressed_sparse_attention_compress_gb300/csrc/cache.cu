@@ -7,11 +7,18 @@
 // max(s_old, s), and when that grew the earlier codes are multiplied by s_old / s
 // (a power of two: exact above E4M3's subnormals).  One item owns its scale and
 // its codes, so nothing is atomic and results do not depend on order.
-// Bound by HBM: each row is read once (kept in registers between the maximum and
-// the conversion) and each code written once.  Few rows per sequence (a decode
-// step) are bound by latency: a warp per item then, 8 items a CTA.
+// Each row is read once (kept in registers between the maximum and the conversion)
+// and each code written once: bound by HBM, once the instructions are few enough.
+// At ten an element (a test for infinities each, 64-bit divisions per item) issue
+// was the bound: 117 us for 16 prompts of 1K to 16K rows (4 heads, K and V, 128
+// dims); with maxima on bf16 pairs as bits and rare infinities apart 81 us, 85% of
+// the rate of a plain copy.  Up to 16 rows a sequence a warp takes an item, 8 items
+// a CTA: 64 sequences with 1, 4, 16 rows 5.0, 3.8, 4.7 us against 7.8, 8.0, 8.7 us.
 //
-// Read.  value = code * scale, one rounding; bound by HBM.
+// Read.  value = code * scale, one rounding; bound by HBM, four bytes written for one
+// read with float32: 46 us for 8 prefixes of 3K to 16K rows (72% of the copy rate).
+// What is left is the look-up of a CTA's rows before its first load; a grid that
+// stays resident and looks the next rows up meanwhile was no faster (48 us).
 #include "cache.cuh"
 
 namespace csa {
@@ -21,7 +28,14 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kKeep = 4;  // 8-element chunks that a thread holds between the two passes
 
-// Eight consecutive elements, as they are stored.
+__device__ __forceinline__ void mul2(float& a, float& b, float m) {  // both products in one instruction
+  asm("{\n .reg .b64 x, y;\n mov.b64 x, {%0, %1};\n mov.b64 y, {%2, %2};\n mul.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}"
+      : "+f"(a), "+f"(b) : "f"(m));
+}
+constexpr uint32_t kInfBits = 0x7f800000u;
+
+// Eight consecutive elements, as they are stored.  top: the largest |x| as float32 bits, which
+// compare like numbers; from kInfBits on, an element is not finite.
 template <typename T> struct Chunk;
 template <> struct Chunk<__nv_bfloat16> {
   uint4 u;
@@ -30,6 +44,15 @@ template <> struct Chunk<__nv_bfloat16> {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[2 * i] = bf16_lo(w[i]), v[2 * i + 1] = bf16_hi(w[i]);
+  }
+  __device__ __forceinline__ uint32_t top() const {
+    const uint32_t a = max2(max2(u.x & 0x7fff7fffu, u.y & 0x7fff7fffu), max2(u.z & 0x7fff7fffu, u.w & 0x7fff7fffu));
+    return max(a << 16, a & 0xffff0000u);
+  }
+  static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t m;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(a), "r"(b));
+    return m;
   }
 };
 template <> struct Chunk<float> {
@@ -41,22 +64,27 @@ template <> struct Chunk<float> {
   __device__ __forceinline__ void get(float (&v)[8]) const {
     v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
   }
+  __device__ __forceinline__ uint32_t top() const {
+    float v[8];
+    get(v);
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+    return m;
+  }
 };
 
 // First slot of sequence b: consecutive sequences are at least as far apart as
 // the blocks that the earlier one's rows can touch.
-__device__ __forceinline__ int64_t slot_base(int32_t cu, int b, int lg) {
-  return ((int64_t)cu >> lg) + 2 * (int64_t)b;
-}
+__device__ __forceinline__ int slot_base(int32_t cu, int b, int lg) { return (cu >> lg) + 2 * b; }
 
 struct Owner {
-  int b, row0, row1, p0;
-  int64_t base;
+  int b, row0, row1, p0, base;
 };
 
 // The last sequence b with slot_base <= slot, by a whole warp: one round of
 // loads up to 31 sequences, 32 ways a round above.
-__device__ __forceinline__ Owner slot_owner(const int32_t* cu, const int32_t* pos0, int B, int lg, int64_t slot,
+__device__ __forceinline__ Owner slot_owner(const int32_t* cu, const int32_t* pos0, int B, int lg, int slot,
                                             int lane) {
   Owner o;
   if (B < 32) {
@@ -84,22 +112,24 @@ __device__ __forceinline__ Owner slot_owner(const int32_t* cu, const int32_t* po
 }
 
 // kWarpItems: a warp per item, 8 items a CTA (few rows per sequence); else a CTA
-// per item, whose threads hold kKeep chunks each of a full block.
+// per item, whose threads hold kKeep chunks each of a full block (four CTAs of 64 rows
+// x 128 dims an SM in bf16: 81 us, with three 83, with the two of 64 registers 104).
 template <typename T, int D, bool kWarpItems>
-__global__ void __launch_bounds__(kWarpItems ? kThreads : 512)
+__global__ void __launch_bounds__(kWarpItems ? kThreads : 512, kWarpItems ? 4 : sizeof(T) == 2 ? 4 : 2)
 cache_write_kernel(CacheView c, const T* __restrict__ x_k, const T* __restrict__ x_v, const int32_t* __restrict__ cu,
-                   const int32_t* __restrict__ pos0, int B, int T_cap, int64_t n_items, int* status) {
+                   const int32_t* __restrict__ pos0, int B, int T_cap, uint32_t n_items, int* status) {
   constexpr int kChunks = D / 8;
-  __shared__ float s_max[16];
+  __shared__ uint32_t s_max[16];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31;
   const int t = kWarpItems ? lane : threadIdx.x, n_t = kWarpItems ? 32 : blockDim.x;
-  const int64_t item = kWarpItems ? (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5) : blockIdx.x;
+  const uint32_t item = kWarpItems ? blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5) : blockIdx.x;
   if (item >= n_items) return;
-  const int kinds = c.v ? 2 : 1;
-  const int h = (int)(item % c.H_kv);
-  const bool is_v = (item / c.H_kv) % kinds != 0;
-  const int64_t slot = item / (c.H_kv * kinds);
+  const uint32_t parts = c.v ? 2 * c.H_kv : c.H_kv;
+  const int slot = (int)(item / parts);
+  int h = (int)(item - slot * parts);
+  const bool is_v = h >= c.H_kv;
+  if (is_v) h -= c.H_kv;
   const int lg = c.log_block, P = 1 << lg;
 
   const Owner o = slot_owner(cu, pos0, B, lg, slot, lane);
@@ -109,8 +139,8 @@ cache_write_kernel(CacheView c, const T* __restrict__ x_k, const T* __restrict__
     if (t == 0) raise_status(status, CSA_ERR_DEVICE_BOUNDS);
     return;
   }
-  const int64_t nth = slot - o.base;
-  const int64_t j = (p0 >> lg) + nth;  // block of the sequence
+  const int nth = slot - o.base;
+  const int64_t j = (int64_t)(p0 >> lg) + nth;  // block of the sequence
   if (nth < 0 || (j << lg) >= (int64_t)p0 + L) return;
   const int first = (int)(j << lg);  // position of the block's first row
   const int lo = max(p0 - first, 0), hi = min(p0 + L - first, P);
@@ -133,27 +163,34 @@ cache_write_kernel(CacheView c, const T* __restrict__ x_k, const T* __restrict__
   float* scale = (is_v ? c.v_scale : c.k_scale) + (int64_t)blk * c.H_kv + h;
   const float old_s = lo > 0 ? *scale : 0.f;
 
-  float amax = 0.f;
+  uint32_t most = 0;     // of the finite elements
+  bool special = false;  // others among this thread's
   for (int base = 0; base < n; base += n_t * kKeep) {
     if (base > 0) load(base);
 #pragma unroll
     for (int k = 0; k < kKeep; ++k) {
       if (base + t + k * n_t < n) {
-        float f[8];
-        v[k].get(f);
+        uint32_t m = v[k].top();
+        if (m >= kInfBits) {
+          special = true;
+          m = 0;
+          float f[8];
+          v[k].get(f);
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (fabsf(f[e]) < INFINITY) amax = fmaxf(amax, fabsf(f[e]));
+          for (int e = 0; e < 8; ++e)
+            if (fabsf(f[e]) < INFINITY) m = max(m, __float_as_uint(fabsf(f[e])));
+        }
+        most = max(most, m);
       }
     }
   }
-#pragma unroll
-  for (int s = 16; s > 0; s >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, s));
+  most = __reduce_max_sync(0xffffffffu, most);
   if (!kWarpItems) {
-    if (lane == 0) s_max[threadIdx.x >> 5] = amax;
+    if (lane == 0) s_max[threadIdx.x >> 5] = most;
     __syncthreads();
-    for (int w = 0; w < (n_t >> 5); ++w) amax = fmaxf(amax, s_max[w]);
+    for (int w = 0; w < (n_t >> 5); ++w) most = max(most, s_max[w]);
   }
+  const float amax = __uint_as_float(most);
   const float need = pow2i(e4m3_scale_exponent(amax));
   const float new_s = lo > 0 ? fmaxf(old_s, need) : need;
 
@@ -183,7 +220,12 @@ cache_write_kernel(CacheView c, const T* __restrict__ x_k, const T* __restrict__
         float f[8];
         v[k].get(f);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = fabsf(f[e]) < INFINITY ? f[e] * inv : NAN;
+        for (int e = 0; e < 8; e += 2) mul2(f[e], f[e + 1], inv);
+        if (special) {  // an infinity becomes NaN; a NaN is one already
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (!(fabsf(f[e]) < INFINITY)) f[e] = NAN;
+        }
         const uint32_t w0 = (uint32_t)e4m3x2_from_floats(f[0], f[1]) | (uint32_t)e4m3x2_from_floats(f[2], f[3]) << 16;
         const uint32_t w1 = (uint32_t)e4m3x2_from_floats(f[4], f[5]) | (uint32_t)e4m3x2_from_floats(f[6], f[7]) << 16;
         *reinterpret_cast<uint2*>(codes + (lo + i / kChunks) * D + (i % kChunks) * 8) = make_uint2(w0, w1);
@@ -194,26 +236,23 @@ cache_write_kernel(CacheView c, const T* __restrict__ x_k, const T* __restrict__
 }
 
 constexpr int kReadRows = 16;  // packed rows of a CTA
+constexpr int kReadAhead = 2;  // chunks of 8 codes that a thread has in flight
 
-template <typename T> __device__ __forceinline__ void store16(T* p, const float (&v)[16]);
-template <> __device__ __forceinline__ void store16<__nv_bfloat16>(__nv_bfloat16* p, const float (&v)[16]) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-    reinterpret_cast<uint4*>(p)[i] =
-        make_uint4(pack_bf16x2(v[8 * i], v[8 * i + 1]), pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
-                   pack_bf16x2(v[8 * i + 4], v[8 * i + 5]), pack_bf16x2(v[8 * i + 6], v[8 * i + 7]));
+template <typename T> __device__ __forceinline__ void store8(T* p, const float (&v)[8]);
+template <> __device__ __forceinline__ void store8<__nv_bfloat16>(__nv_bfloat16* p, const float (&v)[8]) {
+  *reinterpret_cast<uint4*>(p) =
+      make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
 }
-template <> __device__ __forceinline__ void store16<float>(float* p, const float (&v)[16]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    reinterpret_cast<float4*>(p)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+template <> __device__ __forceinline__ void store8<float>(float* p, const float (&v)[8]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
 }
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads)
 cache_read_kernel(CacheView c, const int32_t* __restrict__ cu, const int32_t* __restrict__ pos0, int B, int T_cap,
                   T* __restrict__ k_out, T* __restrict__ v_out, int* status) {
-  constexpr int kChunks = D / 16;
+  constexpr int kChunks = D / 8;
   __shared__ int s_blk[kReadRows], s_row[kReadRows];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int64_t row0 = (int64_t)blockIdx.x * kReadRows;
@@ -237,28 +276,41 @@ cache_read_kernel(CacheView c, const int32_t* __restrict__ cu, const int32_t* __
     s_row[threadIdx.x] = r;
   }
   __syncthreads();
-  const int per_kind = rows * c.H_kv * kChunks;
-  for (int i = threadIdx.x; i < per_kind * (v_out ? 2 : 1); i += kThreads) {
-    const bool is_v = i >= per_kind;
-    const int u = is_v ? i - per_kind : i;
-    const int ch = u % kChunks, h = (u / kChunks) % c.H_kv, rr = u / (kChunks * c.H_kv);
-    const int blk = s_blk[rr];
-    float v[16];
+  const int row_chunks = c.H_kv * kChunks, per_kind = rows * row_chunks, n = v_out ? 2 * per_kind : per_kind;
+  for (int i0 = threadIdx.x; i0 < n; i0 += kThreads * kReadAhead) {  // K's chunks, then V's
+    uint2 q[kReadAhead];
+    float s[kReadAhead];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) v[e] = 0.f;
-    if (blk >= 0) {
-      const int64_t bh = (int64_t)blk * c.H_kv + h;
-      const uint4 q = __ldg(reinterpret_cast<const uint4*>((is_v ? c.v : c.k) + ((bh << c.log_block) + s_row[rr]) * D) + ch);
-      const float s = __ldg((is_v ? c.v_scale : c.k_scale) + bh);
-      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 a = f16x2_to_float2(e4m3x2_to_f16x2((uint16_t)w[e]));
-        const float2 d = f16x2_to_float2(e4m3x2_to_f16x2((uint16_t)(w[e] >> 16)));
-        v[4 * e] = a.x * s, v[4 * e + 1] = a.y * s, v[4 * e + 2] = d.x * s, v[4 * e + 3] = d.y * s;
+    for (int k = 0; k < kReadAhead; ++k) {
+      const int at = i0 + k * kThreads, i = at < per_kind ? at : at - per_kind;
+      q[k] = make_uint2(0, 0);
+      s[k] = 0.f;
+      if (at < n) {
+        const int ch = i % kChunks, rr = i / row_chunks, h = (i - rr * row_chunks) / kChunks, blk = s_blk[rr];
+        if (blk >= 0) {
+          const int64_t bh = (int64_t)blk * c.H_kv + h;
+          q[k] = __ldg(reinterpret_cast<const uint2*>((at < per_kind ? c.k : c.v) +
+                                                      ((bh << c.log_block) + s_row[rr]) * D) + ch);
+          s[k] = __ldg((at < per_kind ? c.k_scale : c.v_scale) + bh);
+        }
       }
     }
-    store16((is_v ? v_out : k_out) + ((row0 + rr) * c.H_kv + h) * D + ch * 16, v);
+#pragma unroll
+    for (int k = 0; k < kReadAhead; ++k) {
+      const int at = i0 + k * kThreads;
+      if (at < n) {
+        const uint32_t w[2] = {q[k].x, q[k].y};
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float2 x = f16x2_to_float2(e4m3x2_to_f16x2((uint16_t)w[e]));
+          const float2 y = f16x2_to_float2(e4m3x2_to_f16x2((uint16_t)(w[e] >> 16)));
+          v[4 * e] = x.x * s[k], v[4 * e + 1] = x.y * s[k], v[4 * e + 2] = y.x * s[k], v[4 * e + 3] = y.y * s[k];
+        }
+        T* out = at < per_kind ? k_out + (int64_t)at * 8 : v_out + (int64_t)(at - per_kind) * 8;
+        store8(out + row0 * c.H_kv * D, v);
+      }
+    }
   }
 }
 
@@ -267,21 +319,21 @@ cudaError_t write_launch(const CacheView& c, const void* x_k, const void* x_v, c
                   int T_cap, int* status, cudaStream_t stream) {
   const int64_t slots = ((int64_t)T_cap >> c.log_block) + 2 * (int64_t)B;
   const int64_t items = slots * c.H_kv * (c.v ? 2 : 1);
+  if (items > INT32_MAX) return cudaErrorInvalidConfiguration;
   const T* k = static_cast<const T*>(x_k);
   const T* v = static_cast<const T*>(x_v);
-  if (T_cap <= 4 * (int64_t)B)
+  if (T_cap <= 16 * (int64_t)B)
     return launch_after(cache_write_kernel<T, D, true>, dim3((unsigned)((items + 7) / 8)), dim3(kThreads), 0, stream,
-                        c, k, v, cu, pos0, B, T_cap, items, status);
+                        c, k, v, cu, pos0, B, T_cap, (uint32_t)items, status);
   return launch_after(cache_write_kernel<T, D, false>, dim3((unsigned)items), dim3((D / 8 << c.log_block) / kKeep), 0,
-                      stream, c, k, v, cu, pos0, B, T_cap, items, status);
+                      stream, c, k, v, cu, pos0, B, T_cap, (uint32_t)items, status);
 }
 
 template <typename T, int D>
 cudaError_t read_launch(const CacheView& c, const int32_t* cu, const int32_t* pos0, int B, int T_cap, void* k_out,
                  void* v_out, int* status, cudaStream_t stream) {
   return launch_after(cache_read_kernel<T, D>, dim3((unsigned)(((int64_t)T_cap + kReadRows - 1) / kReadRows)),
-                      dim3(kThreads), 0, stream, c, cu, pos0, B, T_cap, static_cast<T*>(k_out),
-                      static_cast<T*>(v_out), status);
+                      dim3(kThreads), 0, stream, c, cu, pos0, B, T_cap, static_cast<T*>(k_out), static_cast<T*>(v_out), status);
 }
 
 }  // namespace

@@ -2,29 +2,22 @@
 // (csa_cache_attn_fwd): cached compressed entries (every visible one, or those
 // listed) and a window of cached raw rows in one softmax.
 //
-// Work.  R = 16 or 32 (query, head) rows that read one KV head form an item:
-// 2^lq queries of one sequence x their G heads, or a part of one query's heads
-// when G > R.  An item's keys are cut into tiles of 64; all tiles of all items,
-// in order, are divided evenly among a grid that fills the GPU, so ragged
-// batches and single long sequences load it alike.  An item that one CTA holds
-// whole is written at once; the pieces of the others go to the workspace and a
-// second, small kernel joins them in order (no atomics: the same bits every run).
+// Items of R = 16 or 32 (query, head) rows.
 //
-// A tile.  Each of the four warps takes 16 of its keys through a ring of its own
+// A tile.  Each of the four warps takes 32 of its keys at a time through a ring of its own
 // (cp.async, no CTA-wide barrier): codes are widened to halves in registers
 // (exact), S = Q K^T and O += P V run on m16n8k16 products with float32 sums.
 // A decode step moves 2 d bytes per key and head against 4 d G FLOP, so with up
 // to 16 rows a tile it is bound by HBM, and codes go from shared memory straight
 // into product fragments: a thread's 16 consecutive codes of a K row serve four
 // k-steps (the order of the dims within a product is free), and four V rows are
-// interleaved bytewise before widening.
+// interleaved bytewise before widening.  32 sequences of 2K to 32K rows, 64 heads on 8
+// KV heads: 214 us, 81% of the rate of a plain copy; one sequence of 128K rows, split
+// over the whole GPU, 77 us (52%: the start, and pieces joined by a second kernel).
 //
 // Numbers.  A query row is scaled by a power of two so that its largest element
 // is in [2^14, 2^15): bf16 queries are then exact as halves down to 2^-38 of it.
-// float32 queries and weights go in as two halves (22 bits).  With t = log2
-// scores and V scale 2^e: l = sum 2^(t - m) with m = max t in float32; the value
-// products use w = 2^(t + e - M + 15), M = max(t + e), as halves, so neither the
-// range of the scores nor that of the block scales leaves a half's range.
+// float32 queries and weights go in as two halves (22 bits).
 #include <math.h>
 
 #include "cache_attn.cuh"
@@ -640,11 +633,18 @@ cache_attn_kernel(const CacheAttnArgs a, const Plan pl, float* __restrict__ ws_o
   }
 }
 
-// Two row tiles a CTA where a KV head's queries fill them: more than 16 heads a
-// group, or several queries a sequence (each key is then widened once for 32 rows).
-int row_tiles(int T_cap, int B, int G, bool listed, bool fp32) {
-  return !fp32 && (G > 16 || (!listed && (int64_t)T_cap > 4 * (int64_t)B)) ? 2 : 1;
+// Rows that an item can fill: the heads of a group, and without a list the queries of
+// a sequence on average.  The forms below are for 16, 32, 64 and 128 of them; a larger
+// one widens a key once for more rows, and its empty rows cost what full ones do.
+// Measured, us (16 sequences of 2K to 8K rows, 32 heads, 128 dims, separate V; the next
+// smaller form beside it): 16 rows 57 (32: 73), 32 rows 75 (16: 85, 64: 88), 64 rows 56
+// (32: 74, 128: 72), 128 rows 83 (64: 85), 256 rows 130 (64: 150, 32: 227).  Where V is K
+// (24 sequences of 4K to 25K entries), 32 rows: 55 on mma.sync, 45 as 64 on tcgen05.
+// 64 dims: 16 rows 40 (32: 51), 32 rows 51 (16: 60).
+int64_t rows_of_item(int T_cap, int B, int G, bool listed) {
+  return listed || B <= 0 ? G : ((int64_t)T_cap + B - 1) / B * G;
 }
+int row_tiles(int64_t rows, bool fp32) { return !fp32 && rows > 16 ? 2 : 1; }
 constexpr int ctas_per_sm(int mt) { return mt == 1 ? 3 : 2; }
 
 template <typename T, int D, int MT, bool kShared>
@@ -664,16 +664,14 @@ cudaError_t run(const CacheAttnArgs& a, int sm_count, cudaStream_t stream) {
 }
 
 // Rows of an item on tcgen05 (cache_attn_tc.cu), or 0.
-int tc_rows(int T_cap, int B, int G, int d, bool listed, bool fp32) {
-  if (fp32 || d != 128) return 0;
-  if (!listed && (int64_t)T_cap > 4 * (int64_t)B) return 128;
-  return G > 64 ? 128 : G > 16 ? 64 : 0;
+int tc_rows(int64_t rows, bool shared, int d, bool fp32) {
+  return fp32 || d != 128 || rows <= (shared ? 16 : 32) ? 0 : rows <= 64 ? 64 : 128;
 }
 
 template <typename T, int D>
-cudaError_t choose(const CacheAttnArgs& a, int sm_count, cudaStream_t stream) {
+cudaError_t choose(const CacheAttnArgs& a, int64_t rows, int sm_count, cudaStream_t stream) {
   const bool shared = (a.cmp.k ? a.cmp.v : a.raw.v) == nullptr;
-  if (row_tiles(a.T_cap, a.B, a.H / a.H_kv, a.idx != nullptr, sizeof(T) == 4) == 2) {
+  if (row_tiles(rows, sizeof(T) == 4) == 2) {
     if constexpr (sizeof(T) == 2)
       return shared ? run<T, D, 2, true>(a, sm_count, stream) : run<T, D, 2, false>(a, sm_count, stream);
   }
@@ -694,11 +692,11 @@ size_t cache_attn_workspace(int sm_count, int T_cap, int H, int H_kv, int d) {
 
 cudaError_t launch_cache_attn(const CacheAttnArgs& a, bool fp32, int sm_count, cudaStream_t stream) {
   if (a.T_cap <= 0) return cudaSuccess;
-  const int rows = tc_rows(a.T_cap, a.B, a.H / a.H_kv, a.d, a.idx != nullptr, fp32);
-  if (rows > 0) return launch_cache_attn_tc(a, rows, sm_count, stream);
+  const int64_t rows = rows_of_item(a.T_cap, a.B, a.H / a.H_kv, a.idx != nullptr);
+  if (const int tc = tc_rows(rows, (a.cmp.k ? a.cmp.v : a.raw.v) == nullptr, a.d, fp32)) return launch_cache_attn_tc(a, tc, sm_count, stream);
   if (a.d == 64)
-    return fp32 ? choose<float, 64>(a, sm_count, stream) : choose<__nv_bfloat16, 64>(a, sm_count, stream);
-  return fp32 ? choose<float, 128>(a, sm_count, stream) : choose<__nv_bfloat16, 128>(a, sm_count, stream);
+    return fp32 ? choose<float, 64>(a, rows, sm_count, stream) : choose<__nv_bfloat16, 64>(a, rows, sm_count, stream);
+  return fp32 ? choose<float, 128>(a, rows, sm_count, stream) : choose<__nv_bfloat16, 128>(a, rows, sm_count, stream);
 }
 
 }  // namespace csa
