@@ -124,7 +124,7 @@ cache_attn_kernel(const CacheAttnArgs a, const Plan pl, float* __restrict__ ws_o
 
   if (tid == 0) ws_meta[blockIdx.x] = make_int4(-1, 0, 0, 0);
   split_tiles<kThreads, true>(a, pl, R, &s_ctx, smem, L::kBuf);
-  capacity_rows<T, D, kThreads>(a);
+  capacity_rows<T, D>(a, tid, kThreads);
 
   const uint32_t ring = buf + warp * (kStages * L::kStage);
   uint32_t* rows = reinterpret_cast<uint32_t*>(smem + L::kRows) + warp * (kAhead * kStep);
@@ -659,7 +659,7 @@ cudaError_t run(const CacheAttnArgs& a, int sm_count, cudaStream_t stream) {
   if ((e = launch_after(cache_attn_kernel<T, D, MT, kShared>, dim3(grid), dim3(kThreads), L::kSmem, stream, a, pl,
                         sc.pieces, sc.meta, sc.far)) != cudaSuccess)
     return e;
-  return launch_after(cache_attn_join_kernel<T, D, L::R>, dim3(grid, L::R / kWarps), dim3(kThreads), 0, stream, a, pl,
+  return launch_after(cache_attn_join_kernel<T, D, L::R>, dim3(grid, L::R / kJoinWarps), dim3(32 * kJoinWarps), 0, stream, a, pl,
                       (const float*)sc.pieces, (const int4*)sc.meta);
 }
 

@@ -338,31 +338,33 @@ __device__ __forceinline__ void note_split(const Context* ctx, int row0, int nq,
 }
 
 // Rows that belong to no sequence: zeros, lse -inf.
-template <typename T, int D, int kThreads>
-__device__ __forceinline__ void capacity_rows(const CacheAttnArgs& a) {
+template <typename T, int D>
+__device__ __forceinline__ void capacity_rows(const CacheAttnArgs& a, int t, int n_t) {  // thread t of n_t of the CTA
   const int r0 = max(__ldg(a.cu + a.B), 0);
   T* out = static_cast<T*>(a.out);
-  const int64_t n = ((int64_t)a.T_cap - r0) * a.H, step = (int64_t)gridDim.x * kThreads;
-  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n * (D / 8); i += step) {
+  const int64_t n = ((int64_t)a.T_cap - r0) * a.H, step = (int64_t)gridDim.x * n_t;
+  for (int64_t i = (int64_t)blockIdx.x * n_t + t; i < n * (D / 8); i += step) {
     uint4* o = reinterpret_cast<uint4*>(out + (int64_t)r0 * a.H * D) + i * (sizeof(T) / 2);
     o[0] = make_uint4(0, 0, 0, 0);
     if (sizeof(T) == 4) o[1] = make_uint4(0, 0, 0, 0);
   }
   if (a.lse)
-    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += step)
+    for (int64_t i = (int64_t)blockIdx.x * n_t + t; i < n; i += step)
       a.lse[(int64_t)r0 * a.H + i] = -INFINITY;
 }
 
 // Joins the pieces of the item that begins in CTA blockIdx.x's share and goes on
-// in later ones; a warp per row.
+// in later ones; a warp per row.  Lanes hold the pieces' factors, 32 at a time, so that
+// the rows' loads depend on nothing (one sequence of 128K rows has 57 pieces an item).
+constexpr int kJoinWarps = 4;
 template <typename T, int D, int R>
-__global__ void __launch_bounds__(128)
+__global__ void __launch_bounds__(32 * kJoinWarps)
 cache_attn_join_kernel(const CacheAttnArgs a, const Plan pl, const float* __restrict__ ws_o,
                        const int4* __restrict__ ws_meta) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int4 meta = ws_meta[blockIdx.x];
   if (meta.x < 0) return;
-  const int lane = threadIdx.x & 31, r = blockIdx.y * 4 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5);
   const int G = a.H / a.H_kv, sub = meta.z, first = blockIdx.x, last = meta.w;
   const int kvh = sub / pl.parts, h0 = kvh * G + (sub % pl.parts) * R;
   const int heads = min(kvh * G + G - h0, G > R ? R : G);
@@ -382,15 +384,30 @@ cache_attn_join_kernel(const CacheAttnArgs a, const Plan pl, const float* __rest
   float l = 0.f;
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
   const int d4 = lane % (D / 4);
-#pragma unroll 4
-  for (int k = first; k <= last; ++k) {
-    const float* p = piece(k);
-    const float4 x = *reinterpret_cast<const float4*>(p + r * D + 4 * d4);
-    const float pm = p[R * D + r], pM = p[R * D + R + r], q = p[R * D + 2 * R + r];
-    l += q * ex2(pm - m);
-    const float f = ex2(pM - M);
-    v.x += x.x * f, v.y += x.y * f, v.z += x.z * f, v.w += x.w * f;
+  for (int k0 = first; k0 <= last; k0 += 32) {
+    float f = 0.f;
+    if (k0 + lane <= last) {
+      const float* p = piece(k0 + lane) + R * D + r;
+      f = ex2(p[R] - M);
+      l += p[2 * R] * ex2(p[0] - m);
+    }
+    const int n = min(last - k0 + 1, 32);
+#pragma unroll 1
+    for (int j0 = 0; j0 < n; j0 += 8) {
+      float4 x[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        x[j] = j0 + j < n ? *reinterpret_cast<const float4*>(piece(k0 + j0 + j) + r * D + 4 * d4)
+                          : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float fj = __shfl_sync(0xffffffffu, f, j0 + j);
+        v.x += x[j].x * fj, v.y += x[j].y * fj, v.z += x[j].z * fj, v.w += x[j].w * fj;
+      }
+    }
   }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
   const int at = (meta.x + qi) * a.H + h0 + h;
   if (lane < D / 4) store_out<T>(a, at, D, d4, v, finish_factors(a, at, m, M, l));
 }

@@ -195,7 +195,7 @@ cache_attn_tc_kernel(const CacheAttnArgs a, const Plan pl, float* __restrict__ w
     tc::tmem_relinquish();
   }
   split_tiles<kThreads, false>(a, pl, N, &s_ctx, smem_raw, (int)C::kSmem);
-  capacity_rows<__nv_bfloat16, kDim, kThreads>(a);
+  capacity_rows<__nv_bfloat16, kDim>(a, tid, kThreads);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
@@ -770,7 +770,7 @@ cudaError_t run(const CacheAttnArgs& a, int sm_count, cudaStream_t stream) {
   if ((e = launch_after(cache_attn_tc_kernel<N, kShared>, dim3(sm_count), dim3(kThreads), smem, stream, a, pl,
                         sc.pieces, sc.meta)) != cudaSuccess)
     return e;
-  return launch_after(cache_attn_join_kernel<__nv_bfloat16, kDim, N>, dim3(sm_count, N / 4), dim3(128), 0, stream, a, pl,
+  return launch_after(cache_attn_join_kernel<__nv_bfloat16, kDim, N>, dim3(sm_count, N / kJoinWarps), dim3(32 * kJoinWarps), 0, stream, a, pl,
                       (const float*)sc.pieces, (const int4*)sc.meta);
 }
 
