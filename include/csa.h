@@ -500,9 +500,15 @@ csa_status_t csa_cache_read(csa_handle_t handle, const csa_cache_t* cache,
  * Rows without a candidate: out = 0, lse = sink_h (-inf without a sink).
  * Capacity rows: out = 0, lse = -inf.
  *   q, out [T_cap, H, d] (dtype);  lse [T_cap, H] float32 or NULL;  sink [H] float32 or NULL
- * The scores, the softmax and the sums are float32 on exact cached values;
- * bf16 queries are exact too and the weights enter the value products in 11
- * bits; float32 queries and weights enter the products in 22 bits.
+ * The scores, the softmax and the sums are float32 on exact cached values.
+ * bf16 queries enter the score products exactly, but for elements below 2^-32
+ * of the largest finite one among the queries that a kernel takes together (the
+ * heads of a KV head, neighbouring rows of a sequence); float32 queries in 22
+ * bits.  The weights enter the value products in 11 bits (float32: 22), and
+ * terms below 2^-32 of a row's largest weight times scale are rounded to
+ * multiples of that; l and lse come from the unrounded ones.  A row whose
+ * query is not finite is NaN; other rows do not see it.
+ * out and lse may not overlap the inputs.
  * ws: device scratch of csa_cache_attn_workspace bytes, 16-byte aligned, any
  * contents; calls that may overlap on the GPU need one each.  Results do not
  * depend on what is in it and are the same from run to run.

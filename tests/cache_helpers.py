@@ -82,20 +82,22 @@ class Model:
         blk = np.asarray(self.table[b])[pos // self.block]
         return VALUES[self.codes[blk, :, pos % self.block]] * self.scale[blk][:, :, None]
 
+    def scales(self, b, pos):
+        return self.scale[np.asarray(self.table[b])[np.asarray(pos, np.int64) // self.block]]
+
 
 def attend(q, cu, pos0, scale, cmp=None, raw=None, idx=None, base=None, ratio=0, window=0, sink=None):
-    """(out, lse, bound_out, bound_lse) of attention over Models given as (K, V) pairs, in float64.
-    The bounds are those of the rounding of the kernels' float32 arithmetic, without the output's
-    own rounding and without that of the weights; A = sum of p |V| is returned for the latter."""
+    """(out, lse, mass, ds, low) of attention over Models given as (K, V) pairs, in float64, for check():
+    mass = sum of p |V|, ds the error of a score in float32, low that of weights below a half's range."""
     T, H, d = q.shape
     out, lse = np.zeros((T, H, d)), np.full((T, H), -math.inf)
-    mass, ds = np.zeros((T, H, d)), np.zeros((T, H))
+    mass, ds, low = np.zeros((T, H, d)), np.zeros((T, H)), np.zeros((T, H, d))
     hk = (cmp or raw)[0].codes.shape[1]
     G = H // hk
     for b in range(len(cu) - 1):
         for t in range(cu[b], cu[b + 1]):
             p = pos0[b] + t - cu[b]
-            ks, vs = [], []
+            ks, vs, ss = [], [], []
             if cmp is not None:
                 vis = (p + 1) // ratio
                 e = np.arange(vis)
@@ -105,11 +107,13 @@ def attend(q, cu, pos0, scale, cmp=None, raw=None, idx=None, base=None, ratio=0,
                     e = e[(e >= 0) & (e < vis)]
                 ks.append(cmp[0].rows(b, e))
                 vs.append(cmp[1].rows(b, e))
+                ss.append(cmp[1].scales(b, e))
             if raw is not None:
                 w = np.arange(max(0, p - window + 1), p + 1)
                 ks.append(raw[0].rows(b, w))
                 vs.append(raw[1].rows(b, w))
-            K, V = np.concatenate(ks), np.concatenate(vs)
+                ss.append(raw[1].scales(b, w))
+            K, V, S = np.concatenate(ks), np.concatenate(vs), np.concatenate(ss)
             n = len(K)
             for h in range(H):
                 x = (K[:, h // G] @ q[t, h]) * scale
@@ -123,22 +127,26 @@ def attend(q, cu, pos0, scale, cmp=None, raw=None, idx=None, base=None, ratio=0,
                     continue
                 out[t, h] = (e @ V[:, h // G]) / z
                 mass[t, h] = (e @ np.abs(V[:, h // G])) / z
+                # V = code s; the products take codes, with weights p s in halves, the largest of them as 2^7 or
+                # more.  Halves below 2^-14 are multiples of 2^-24: an error of up to 2^-25 a key, 2^-32 of the largest.
+                ps = e * S[:, h // G]
+                low[t, h] = 2.0 ** -32 * np.max(ps) / z * (np.abs(V[:, h // G]) / S[:, h // G][:, None]).sum(0)
                 # a score: d products summed in float32, then scaled, taken to log2 units and reduced
                 dot = scale * float(np.max(np.abs(K[:, h // G]) @ np.abs(q[t, h])))
                 ds[t, h] = 2.0 ** -24 * ((d + 4) * dot + 4 * float(np.max(np.abs(x)) + abs(top)) + n + 16)
-    return out, lse, mass, ds
+    return out, lse, mass, ds, low
 
 
 def check(got, got_lse, ref, q_dtype):
     """The kernel's outputs against attend()'s: each rounding counted once."""
-    out, lse, mass, ds = ref
+    out, lse, mass, ds, low = ref
     g = got.double().cpu().numpy()
     assert np.array_equal(np.isnan(g), np.isnan(out))
     # weights 11 bits for bf16 queries (half a step: 2^-11), 22 bits for float32 (hi + lo halves: 2^-21 with the
     # queries' own); a relative error of 2 ds in the weights from the scores and the sum
     w = 2.0 ** -11 if q_dtype == torch.bfloat16 else 2.0 ** -21
     own = 2.0 ** -8 if q_dtype == torch.bfloat16 else 2.0 ** -23
-    bound = own * np.abs(out) + (w + 4 * ds[..., None]) * mass * 1.01 + 1e-37
+    bound = own * np.abs(out) + (w + 4 * ds[..., None]) * mass * 1.01 + low + 1e-37
     bad = np.abs(g - out) > bound
     assert not bad[~np.isnan(out)].any(), float(np.nanmax((np.abs(g - out) / bound)))
     if got_lse is not None:

@@ -36,7 +36,7 @@ def test_attention_model_is_torchs():
     s = ch.Setup(0, 1, [40], 2, 64, 16, False, device="cpu")
     k, v = s.models()
     q = np.random.default_rng(1).standard_normal((1, 4, 64))
-    out, lse, _, _ = ch.attend(q, [0, 1], [39], 0.125, raw=(k, v), window=100)
+    out, lse, *_ = ch.attend(q, [0, 1], [39], 0.125, raw=(k, v), window=100)
     K, V = (torch.from_numpy(m.rows(0, range(40))).repeat_interleave(2, 1).transpose(0, 1) for m in (k, v))
     ref = torch.nn.functional.scaled_dot_product_attention(torch.from_numpy(q).transpose(0, 1), K, V)
     np.testing.assert_allclose(out[0], ref[:, 0], rtol=1e-10, atol=1e-12)
