@@ -281,7 +281,7 @@ cache_attn_tc_kernel(const CacheAttnArgs a, const Plan pl, float* __restrict__ w
 
       // the item's queries
       const uint32_t qb = n_item % C::kQBufs;
-      bool ok = mbar_wait_bounded(smem_u32(&s_qempty[qb]), (n_item / C::kQBufs & 1u) ^ 1u, status);
+      bool ok = true;
       float qf;
       {
         auto query = [&](int at) -> uint4 {  // 8 dims of row at / 16
@@ -307,7 +307,8 @@ cache_attn_tc_kernel(const CacheAttnArgs a, const Plan pl, float* __restrict__ w
           s_qmax[n_item & 1u][w] = amax;
           mbar_arrive(smem_u32(&s_qmaxed));
         }
-        ok = ok && mbar_wait_bounded(smem_u32(&s_qmaxed), n_item & 1u, status);
+        ok = mbar_wait_bounded(smem_u32(&s_qmaxed), n_item & 1u, status) &&
+             mbar_wait_bounded(smem_u32(&s_qempty[qb]), (n_item / C::kQBufs & 1u) ^ 1u, status);
         if ((dead = __any_sync(0xffffffffu, !ok))) break;
 #pragma unroll
         for (int i = 0; i < kConvWarps; ++i) amax = fmaxf(amax, s_qmax[n_item & 1u][i]);
@@ -760,8 +761,8 @@ cache_attn_tc_kernel(const CacheAttnArgs a, const Plan pl, float* __restrict__ w
 template <int N, bool kShared>
 cudaError_t run(const CacheAttnArgs& a, int sm_count, cudaStream_t stream) {
   using C = Tc<N, kShared>;
-  // an item costs as much as 2 or 4 tiles beside its own (prompt chunks: 444 us with 0, 399 us so)
-  const Plan pl = make_plan(a, N, N == 128 ? 2 : 4);
+  // an item costs as much as 6 or 4 tiles beside its own (prompt chunks: 444 us with 0, 396 with 2, 353 so, 368 with 14)
+  const Plan pl = make_plan(a, N, N == 128 ? 6 : 4);
   const Scratch sc = scratch_of<kDim>(a.ws, sm_count, N);
   const size_t smem = C::kSmem + 1024;
   cudaError_t e = cudaFuncSetAttribute(cache_attn_tc_kernel<N, kShared>, cudaFuncAttributeMaxDynamicSharedMemorySize,
