@@ -13,7 +13,7 @@
 // was the bound: 117 us for 16 prompts of 1K to 16K rows (4 heads, K and V, 128
 // dims); with maxima on bf16 pairs as bits and rare infinities apart 81 us, 85% of
 // the rate of a plain copy.  Up to 16 rows a sequence a warp takes an item, 8 items
-// a CTA: 64 sequences with 1, 4, 16 rows 5.0, 3.8, 4.7 us against 7.8, 8.0, 8.7 us.
+// a CTA: 64 sequences with 1, 4, 16 rows 5 to 6 us against 7.7, 7.9, 8.8 us.
 //
 // Read.  value = code * scale, one rounding; bound by HBM, four bytes written for one
 // read with float32: 46 us for 8 prefixes of 3K to 16K rows (72% of the copy rate).

@@ -12,8 +12,8 @@
 // into product fragments: a thread's 16 consecutive codes of a K row serve four
 // k-steps (the order of the dims within a product is free), and four V rows are
 // interleaved bytewise before widening.  32 sequences of 2K to 32K rows, 64 heads on 8
-// KV heads: 214 us, 81% of the rate of a plain copy; one sequence of 128K rows, split
-// over the whole GPU, 77 us (52%: the start, and pieces joined by a second kernel).
+// KV heads: 204 us, 84% of the rate of a plain copy; one sequence of 128K rows, split
+// over the whole GPU, 71 us (56%: the start, and pieces joined by a second kernel).
 //
 // Numbers.  A query row is scaled by a power of two so that its largest element
 // is in [2^14, 2^15): bf16 queries are then exact as halves down to 2^-38 of it.
@@ -636,11 +636,13 @@ cache_attn_kernel(const CacheAttnArgs a, const Plan pl, float* __restrict__ ws_o
 // Rows that an item can fill: the heads of a group, and without a list the queries of
 // a sequence on average.  The forms below are for 16, 32, 64 and 128 of them; a larger
 // one widens a key once for more rows, and its empty rows cost what full ones do.
-// Measured, us (16 sequences of 2K to 8K rows, 32 heads, 128 dims, separate V; the next
-// smaller form beside it): 16 rows 57 (32: 73), 32 rows 75 (16: 85, 64: 88), 64 rows 56
-// (32: 74, 128: 72), 128 rows 83 (64: 85), 256 rows 130 (64: 150, 32: 227).  Where V is K
-// (24 sequences of 4K to 25K entries), 32 rows: 55 on mma.sync, 45 as 64 on tcgen05.
-// 64 dims: 16 rows 40 (32: 51), 32 rows 51 (16: 60).
+// Measured, us, with separate V (16 sequences of 2K to 8K rows, 32 heads, 128 dims; 16 and
+// 32 rows on mma.sync, 64 and 128 on tcgen05), by the rows that there are:
+//    16: 53 (as 32: 69, as 64: 88)     32: 71 (as 16: 82, as 64: 89)
+//    64: 57 (as 32: 70, as 128: 76)   128: 81 (as 64: 87)   256: 129 (as 64: 154, as 32: 217)
+// where V is K (24 sequences of 4K to 25K entries): 16: 38 (as 64: 43), 32: as 64 44 (as 32: 47);
+// 512 listed entries of 48 sequences: 16: 21.3 (as 64: 22.3), 32: as 64 23.5 (as 32: 23.7);
+// 64 dims: 16: 38 (as 32: 49), 32: 49 (as 16: 60).
 int64_t rows_of_item(int T_cap, int B, int G, bool listed) {
   return listed || B <= 0 ? G : ((int64_t)T_cap + B - 1) / B * G;
 }

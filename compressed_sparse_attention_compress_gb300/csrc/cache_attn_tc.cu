@@ -2,9 +2,12 @@
 // cores: 128 dims, bf16 queries, many (query, head) rows per KV head (64 shared
 // heads of a decode step, or the queries of a chunk).
 //
-// With 64 rows a key takes 64 x 4 x 128 FLOP against its 128 to 256 bytes: tensor
-// pipe and instruction issue bound this form, not HBM.  Tiles are transposed as in
-// the training kernels, the 128 keys on the lanes of tensor memory:
+// With 64 rows a key takes 64 x 4 x 128 FLOP against its 128 to 256 bytes: what bounds
+// this form is neither HBM nor the tensor pipe (16% busy in prompt chunks, 373 TFLOP/s
+// there, 290 in dense decode) but the softmax's chain of dependent steps per tile (loads
+// from tensor memory, a vote, exponentials, P^T, a barrier) and, in small calls, the first
+// pass through the code.  Tiles are transposed as in the training kernels, the 128 keys on
+// the lanes of tensor memory:
 //   S^T[key, r]  = K[key, :] . Q[r, :]        (M = 128, N = 64 or 128, K = 128 dims)
 //   O^T[dim, r] += V^T[dim, key] P^T[key, r]  (M = 128, N, K = 128 keys)
 // so a thread owns a key: its block scales and its place in the mask are scalars.
@@ -275,6 +278,20 @@ cache_attn_tc_kernel(const CacheAttnArgs a, const Plan pl, float* __restrict__ w
         }
       };
       Unit uk, uv;
+      auto query = [&](int at) -> uint4 {  // 8 dims of row at / 16
+        const int r = at >> 4, qi = G > N ? 0 : r / G, h = G > N ? r : r % G;
+        if (qi >= it.x.nq || h >= it.heads) return make_uint4(0, 0, 0, 0);
+        return __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
+                                                    ((int64_t)(it.x.row0 + qi) * a.H + it.h0 + h) * kDim) + (at & 15));
+      };
+      // 64 rows stay in registers between the maximum and the products' form (a call for one token: 18.0 -> 16.8 us);
+      // 128 are read twice
+      constexpr int kIter = N * 16 / kConvThreads;
+      uint4 held[N == 64 ? kIter : 1];
+      if (N == 64) {
+#pragma unroll
+        for (int i = 0; i < kIter; ++i) held[N == 64 ? i : 0] = query(ct + i * kConvThreads);
+      }
       look_up(t0);
       load(uk, t0, false);
       if (!kShared) load(uv, t0, true);
@@ -284,16 +301,10 @@ cache_attn_tc_kernel(const CacheAttnArgs a, const Plan pl, float* __restrict__ w
       bool ok = true;
       float qf;
       {
-        auto query = [&](int at) -> uint4 {  // 8 dims of row at / 16
-          const int r = at >> 4, qi = G > N ? 0 : r / G, h = G > N ? r : r % G;
-          if (qi >= it.x.nq || h >= it.heads) return make_uint4(0, 0, 0, 0);
-          return __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
-                                                      ((int64_t)(it.x.row0 + qi) * a.H + it.h0 + h) * kDim) + (at & 15));
-        };
         float amax = 0.f;
-#pragma unroll 2
-        for (int at = ct; at < N * 16; at += kConvThreads) {
-          const uint4 u = query(at);
+#pragma unroll(N == 64 ? kIter : 4)
+        for (int i = 0; i < kIter; ++i) {
+          const uint4 u = N == 64 ? held[N == 64 ? i : 0] : query(ct + i * kConvThreads);
           const uint32_t v[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -316,9 +327,10 @@ cache_attn_tc_kernel(const CacheAttnArgs a, const Plan pl, float* __restrict__ w
         const float mul = a.scale < 0.f ? -pow2i(-ex) : pow2i(-ex);
         qf = pow2i(ex) * fabsf(a.scale) * kLog2e;
         const uint32_t to = base + C::kQOff + qb * C::kQBytes;
-#pragma unroll 2
-        for (int at = ct; at < N * 16; at += kConvThreads) {
-          const uint4 u = query(at);
+#pragma unroll(N == 64 ? kIter : 2)
+        for (int i = 0; i < kIter; ++i) {
+          const int at = ct + i * kConvThreads;
+          const uint4 u = N == 64 ? held[N == 64 ? i : 0] : query(at);
           sts128(to + ((at & 15) >> 3) * C::kQRegion + tc::sw128_offset(at >> 4, at & 7),
                  pack_f16x2(bf16_lo(u.x) * mul, bf16_hi(u.x) * mul), pack_f16x2(bf16_lo(u.y) * mul, bf16_hi(u.y) * mul),
                  pack_f16x2(bf16_lo(u.z) * mul, bf16_hi(u.z) * mul), pack_f16x2(bf16_lo(u.w) * mul, bf16_hi(u.w) * mul));
@@ -761,7 +773,7 @@ cache_attn_tc_kernel(const CacheAttnArgs a, const Plan pl, float* __restrict__ w
 template <int N, bool kShared>
 cudaError_t run(const CacheAttnArgs& a, int sm_count, cudaStream_t stream) {
   using C = Tc<N, kShared>;
-  // an item costs as much as 6 or 4 tiles beside its own (prompt chunks: 444 us with 0, 396 with 2, 353 so, 368 with 14)
+  // an item costs as much as 6 or 4 tiles beside its own (prompt chunks: 444 us with 0, 396 with 2, 354 so, 368 with 14)
   const Plan pl = make_plan(a, N, N == 128 ? 6 : 4);
   const Scratch sc = scratch_of<kDim>(a.ws, sm_count, N);
   const size_t smem = C::kSmem + 1024;
