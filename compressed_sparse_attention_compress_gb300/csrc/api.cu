@@ -432,7 +432,7 @@ csa_status_t cache_view(const csa_cache_t* c, csa::CacheView* out) {
   if (!aligned16(c->k) || !opt_aligned16(c->v) || !aligned4(c->k_scale) || !aligned4(c->v_scale) ||
       !aligned4(c->table))
     return CSA_ERR_INVALID_ARG;
-  if (!pow2_in(c->block, 16, 128) || (c->d != 64 && c->d != 128)) return CSA_ERR_UNSUPPORTED;
+  if (!pow2_in(c->block, 16, 128) || (c->d != 64 && c->d != 128) || c->H_kv > 65536) return CSA_ERR_UNSUPPORTED;
   if ((int64_t)c->max_blocks * c->block > (1 << 30) || (int64_t)c->n_blocks * c->H_kv > INT32_MAX ||
       (int64_t)c->n_blocks * c->H_kv * c->block > UINT32_MAX - 1)
     return CSA_ERR_UNSUPPORTED;
@@ -458,6 +458,8 @@ csa_status_t csa_cache_write(csa_handle_t h, const csa_cache_t* cache, const voi
   if (!x_k || !pos0 || (x_v != nullptr) != (c.v != nullptr) || !aligned16(x_k) || !opt_aligned16(x_v) || !aligned4(cu) ||
       !aligned4(pos0))
     return CSA_ERR_INVALID_ARG;
+  // one number for every block that the rows may touch, head, and K or V
+  if ((((int64_t)T_cap >> c.log_block) + 2 * (int64_t)B) * c.H_kv * (c.v ? 2 : 1) > INT32_MAX) return CSA_ERR_UNSUPPORTED;
   DeviceGuard g(h->device);
   if (!g.ok) return CSA_ERR_CUDA;
   return from_cuda(csa::launch_cache_write(c, x_k, x_v, cu, pos0, B, T_cap, dtype == CSA_FP32, h->status, stream));
@@ -470,8 +472,8 @@ csa_status_t csa_cache_read(csa_handle_t h, const csa_cache_t* cache, const int3
   const csa_status_t st = cache_view(cache, &c);
   if (st != CSA_OK) return st;
   if (T_cap == 0) return CSA_OK;
-  if (!k_out || (B > 0 && !pos0) || (v_out != nullptr && c.v == nullptr) || !aligned16(k_out) || !opt_aligned16(v_out) || !aligned4(cu) ||
-      !aligned4(pos0))
+  if (!k_out || (B > 0 && !pos0) || (v_out != nullptr && c.v == nullptr) || !aligned16(k_out) ||
+      !opt_aligned16(v_out) || !aligned4(cu) || !aligned4(pos0))
     return CSA_ERR_INVALID_ARG;
   DeviceGuard g(h->device);
   if (!g.ok) return CSA_ERR_CUDA;
@@ -507,7 +509,6 @@ csa_status_t csa_cache_attn_fwd(csa_handle_t h, const void* q, const csa_cache_t
   a.q = q; a.idx = idx; a.k_pad = k_pad; a.cu_cmp = cu_cmp; a.sink = sink; a.cu = cu; a.pos0 = pos0;
   a.B = B; a.T_cap = T_cap; a.H = H; a.H_kv = c.H_kv; a.d = d; a.r = ratio;
   a.window = window < (1 << 30) ? window : 1 << 30;  // no cache is longer
- 
   a.scale = softmax_scale; a.out = out; a.lse = lse; a.ws = ws; a.status = h->status;
   DeviceGuard g(h->device);
   if (!g.ok) return CSA_ERR_CUDA;

@@ -319,7 +319,6 @@ cudaError_t write_launch(const CacheView& c, const void* x_k, const void* x_v, c
                   int T_cap, int* status, cudaStream_t stream) {
   const int64_t slots = ((int64_t)T_cap >> c.log_block) + 2 * (int64_t)B;
   const int64_t items = slots * c.H_kv * (c.v ? 2 : 1);
-  if (items > INT32_MAX) return cudaErrorInvalidConfiguration;
   const T* k = static_cast<const T*>(x_k);
   const T* v = static_cast<const T*>(x_v);
   if (T_cap <= 16 * (int64_t)B)

@@ -452,7 +452,7 @@ typedef struct csa_cache_s {
   int n_blocks, max_blocks;  /* max_blocks * block at most 2^30; n_blocks * H_kv
                                below 2^31 and times block below 2^32 - 1 */
   int block;             /* rows of a block: 16, 32, 64 or 128 */
-  int H_kv, d;           /* d 64 or 128 */
+  int H_kv, d;           /* H_kv at most 65536; d 64 or 128 */
 } csa_cache_t;
 
 /* Quantise rows into a cache as they arrive.  Packed row cu_seqlens[b] + i of
@@ -471,7 +471,8 @@ typedef struct csa_cache_s {
  * Only one sequence may write to a block in one call.  A sequence whose
  * positions are negative or reach past max_blocks * block, and a block number
  * out of range, raise CSA_ERR_DEVICE_BOUNDS and are skipped.
- * H_kv >= 1; other block, d: CSA_ERR_UNSUPPORTED. */
+ * Other block, d or sizes: CSA_ERR_UNSUPPORTED; so are calls where
+ * (T_cap / block + 2 B) * H_kv (twice that with V) reaches 2^31. */
 csa_status_t csa_cache_write(csa_handle_t handle, const csa_cache_t* cache, const void* x_k,
                              const void* x_v, const int32_t* cu_seqlens, const int32_t* pos0,
                              int B, int T_cap, csa_dtype_t dtype, cudaStream_t stream);

@@ -109,6 +109,12 @@ def test_host_refusals_of_the_attention():
     assert api.LIB.csa_cache_attn_workspace(None, 4, 4, 1, 64) == 0
 
 
+def test_host_refusals_of_sizes():
+    assert _write(_struct(H_kv=65537, n_blocks=1)) == -2
+    assert _write(_struct(H_kv=65536, n_blocks=1), B=20000, T=1 << 20) == -2   # 105,536 blocks x 65,536 heads
+    assert _attn(raw=_struct(H_kv=65537, n_blocks=1), window=4, H=65537) == -2
+
+
 def test_python_checks():
     import pytest
     with pytest.raises(ValueError):

@@ -144,6 +144,49 @@ def test_many_ragged_sequences(H, H_kv, shared, n):
     c.check()
 
 
+@pytest.mark.parametrize("H,d,fp32", [(2, 64, True), (4, 128, False), (17, 128, False)])
+def test_more_sequences_than_shared_memory_holds(H, d, fp32):
+    # items of one tile, which no CTA cuts: the same bits as in calls of 2000 sequences
+    B, block, n = 26000, 16, 64
+    g = torch.Generator().manual_seed(4)
+    k = torch.randint(0, 0x7E, (n, 1, block, d), generator=g, dtype=torch.uint8).cuda()
+    ks = torch.full((n, 1), 2.0 ** -7, device="cuda")
+    table = torch.randint(0, n, (B, 4), generator=g, dtype=torch.int32).cuda()
+    ctx = torch.randint(0, 60, (B,), generator=g, dtype=torch.int32).cuda()
+    dt = torch.float32 if fp32 else torch.bfloat16
+    q = torch.randn(B + 5, H, d, generator=g).cuda().to(dt)
+    h = api.Handle(0)
+
+    def run(lo, hi, rows):
+        out = torch.full_like(rows, 3.0)
+        ws = torch.empty(api.csa_cache_attn_workspace(h, len(rows), H, 1, d), dtype=torch.uint8, device="cuda")
+        api.csa_cache_attn_fwd(h, rows, _i32(np.arange(hi - lo + 1)), ctx[lo:hi].clone(), d ** -0.5, out, ws,
+                               raw=api.Cache(k, ks, table[lo:hi].clone()), window=FULL)
+        return out
+
+    whole = run(0, B, q)
+    for lo in range(0, B, 2000):
+        assert torch.equal(whole[lo:lo + 2000], run(lo, lo + 2000, q[lo:lo + 2000].clone()))
+    assert not whole[B:].any() and h.device_status() == 0
+
+
+def test_no_sequences():
+    c = call("64_shared", 1, pad=6)
+    none = _i32([0])
+    empty = torch.empty(0, dtype=torch.int32, device="cuda")
+    x = c.q[:, :1].contiguous()
+    before = c.raw.k.clone()
+    api.csa_cache_write(c.h, c.raw, x, none, empty)
+    api.csa_cache_read(c.h, c.raw, none, empty, x)
+    api.csa_cache_attn_fwd(c.h, c.q, none, empty, c.scale, c.out, c.ws, raw=c.raw, window=FULL, lse=c.lse)
+    assert c.h.device_status() == 0
+    assert torch.equal(before, c.raw.k) and not x.any() and not c.out.any() and torch.isneginf(c.lse).all()
+    nothing = c.q[:0].contiguous()
+    c.out.fill_(2.0)
+    api.csa_cache_attn_fwd(c.h, nothing, none, empty, c.scale, nothing, None, raw=c.raw, window=FULL)
+    assert c.h.device_status() == 0 and (c.out == 2.0).all()
+
+
 def test_items_cut_among_ctas_and_whole_ones_agree():
     # the same query and cache alone (cut into pieces) and among many (whole): the same values up to the joins
     for H, H_kv, shared in ((8, 1, False), (64, 1, True)):
