@@ -52,7 +52,9 @@ constexpr uint32_t kRegion = kTile * 128;   // 128 keys x 64 halves
 constexpr uint32_t kTileBytes = 2 * kRegion;
 
 template <int N, bool kShared> struct Tc {
-  static constexpr int kStK = kShared ? 3 : 2;                  // K (or K = V) tiles
+  // K (or K = V) tiles, as many as fit: dense decode 51.3 us with three, 50.0 with four (two tiles' codes
+  // on their way in registers instead of one: slower again, 50.9)
+  static constexpr int kStK = kShared ? (N == 64 ? 4 : 3) : 2;
   static constexpr int kStV = kShared ? 0 : 2;
   static constexpr int kQBufs = N == 128 && !kShared ? 1 : 2;
   static constexpr uint32_t kQRegion = N * 128;                 // N rows x 64 halves
