@@ -639,14 +639,14 @@ cache_attn_kernel(const CacheAttnArgs a, const Plan pl, float* __restrict__ ws_o
 // Measured, us, with separate V (16 sequences of 2K to 8K rows, 32 heads, 128 dims; 16 and
 // 32 rows on mma.sync, 64 and 128 on tcgen05), by the rows that there are:
 //    16: 53 (as 32: 69, as 64: 88)     32: 71 (as 16: 82, as 64: 89)
-//    64: 57 (as 32: 70, as 128: 76)   128: 81 (as 64: 87)   256: 129 (as 64: 154, as 32: 217)
-// where V is K (24 sequences of 4K to 25K entries): 16: 38 (as 64: 43), 32: as 64 44 (as 32: 47);
-// 512 listed entries of 48 sequences: 16: 21.3 (as 64: 22.3), 32: as 64 23.5 (as 32: 23.7);
+//    64: 53 (as 32: 70, as 128: 76)   128: 80 (as 64: 86)   256: 127 (as 64: 154, as 32: 217)
+// where V is K (24 sequences of 4K to 25K entries): 16: 38 (as 64: 43), 32: as 64 42 (as 32: 47);
+// 512 listed entries of 48 sequences: 16: 21.3 (as 64: 22.3), 32: as 64 22.5 (as 32: 23.7);
 // 64 dims: 16: 38 (as 32: 49), 32: 49 (as 16: 60).
 int64_t rows_of_item(int T_cap, int B, int G, bool listed) {
   return listed || B <= 0 ? G : ((int64_t)T_cap + B - 1) / B * G;
 }
-int row_tiles(int64_t rows, bool fp32) { return !fp32 && rows > 16 ? 2 : 1; }
+int row_tiles(int64_t rows) { return rows > 16 ? 2 : 1; }  // bf16; float32 has one, in two halves
 constexpr int ctas_per_sm(int mt) { return mt == 1 ? 3 : 2; }
 
 template <typename T, int D, int MT, bool kShared>
@@ -675,9 +675,11 @@ int tc_rows(int64_t rows, bool shared, int d, bool fp32) {
 template <typename T, int D>
 cudaError_t choose(const CacheAttnArgs& a, int64_t rows, int sm_count, cudaStream_t stream) {
   const bool shared = (a.cmp.k ? a.cmp.v : a.raw.v) == nullptr;
-  if (row_tiles(rows, sizeof(T) == 4) == 2) {
-    if constexpr (sizeof(T) == 2)
-      return shared ? run<T, D, 2, true>(a, sm_count, stream) : run<T, D, 2, false>(a, sm_count, stream);
+  if constexpr (sizeof(T) == 2) {
+    if (row_tiles(rows) == 2) {
+      if (!shared) return run<T, D, 2, false>(a, sm_count, stream);
+      if constexpr (D == 64) return run<T, D, 2, true>(a, sm_count, stream);  // 128 dims: on tcgen05
+    }
   }
   return shared ? run<T, D, 1, true>(a, sm_count, stream) : run<T, D, 1, false>(a, sm_count, stream);
 }

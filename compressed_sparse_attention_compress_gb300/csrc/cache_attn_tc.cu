@@ -4,7 +4,7 @@
 //
 // With 64 rows a key takes 64 x 4 x 128 FLOP against its 128 to 256 bytes: what bounds
 // this form is neither HBM nor the tensor pipe (18% busy in prompt chunks, 420 TFLOP/s
-// there, 290 in dense decode) but the softmax's chain of dependent steps per tile (loads
+// there, 300 in dense decode) but the softmax's chain of dependent steps per tile (loads
 // from tensor memory, a vote, exponentials, P^T, a barrier) and, in small calls, the first
 // pass through the code.  Tiles are transposed as in the training kernels, the 128 keys on
 // the lanes of tensor memory:
